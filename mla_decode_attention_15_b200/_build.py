@@ -34,7 +34,7 @@ def _nvcc() -> str:
 
 
 def sources() -> list:
-    return sorted(glob.glob(os.path.join(PKG, "csrc", "*"))) + [os.path.join(INCLUDE, "mla_decode.h")]
+    return sorted(glob.glob(os.path.join(PKG, "csrc", "*"))) + sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def up_to_date() -> bool:

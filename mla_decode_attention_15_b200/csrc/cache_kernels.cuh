@@ -1,0 +1,759 @@
+// Kernels around the paged latent cache: rotary positions, the write of new rows
+// (bf16, or e4m3 with one power-of-two scale per page), and the fork, free, copy
+// and compaction of pages (include/mla_cache.h).
+//
+// All of them move bytes: their floor is the data read once and written once,
+// and for the small calls the launch.  None lets a dependent grid start early,
+// and each ends with a device-wide fence, so a decode kernel that reads the
+// cache, the table or the lengths before its own wait on the previous grid
+// reads what these kernels wrote.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cfloat>
+#include <cstdint>
+
+#include "mla_cache.h"
+#include "schedule.cuh"
+#include "sm100_ptx.cuh"
+
+namespace mla {
+
+constexpr int kRopePairs = 32;
+constexpr int kMoveThreads = 256;
+
+// ------------------------------------------------------------------ e4m3
+// Two e4m3 values of (lo, hi), lo in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t h2_of_e4m3x2(uint32_t v) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
+    return r;
+}
+__device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
+__device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
+
+// Exponent e of the power-of-two scale of a largest magnitude amax (its bits;
+// finite, > 0): the least e with amax <= 448 * 2^e.  448 = 1.75 * 2^8.
+__host__ __device__ __forceinline__ int e4m3_scale_exp(uint32_t amax_bits) {
+    return static_cast<int>(amax_bits >> 23) - 127 - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+}
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
+
+constexpr uint32_t kInfBits = 0x7f800000u;
+constexpr int kMinScaleExp = -100, kMaxScaleExp = 119;
+
+// ------------------------------------------------------------------ rotation
+// cos and sin (times the amplitude) of pair i at a position.  The angle in
+// turns is a product of 53-bit numbers, so its fraction is good to 2^-53 of the
+// whole turns: 1e-7 turns are not reached below 2^29 turns.
+__device__ __forceinline__ float2 rope_cos_sin(const double* turns, float amplitude, int pos, int i) {
+    const double t = static_cast<double>(pos) * turns[i];
+    float s, c;
+    sincospif(2.0f * static_cast<float>(t - rint(t)), &s, &c);
+    return make_float2(c * amplitude, s * amplitude);
+}
+__device__ __forceinline__ void rotate(float& a, float& b, float2 cs) {
+    const float x = a * cs.x - b * cs.y, y = a * cs.y + b * cs.x;
+    a = x;
+    b = y;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        f[2 * e] = __uint_as_float(w[e] << 16);
+        f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+
+struct RopeParams {
+    const void* x;
+    const int32_t* positions;
+    void* out;
+    int64_t xt, xh, ot, oh;  // strides in values
+    int T, h, width, offset, transpose;
+    int tpc, hpc;            // tokens and heads per CTA
+    int in_place;
+    mla_rope_table table;
+};
+
+// 8 consecutive columns, as loaded.
+template <typename E>
+struct Chunk8;
+template <>
+struct Chunk8<__nv_bfloat16> {
+    uint4 v;
+    __device__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+    __device__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
+    __device__ void get(float (&f)[8]) const { unpack8(v, f); }
+    __device__ void set(const float (&f)[8]) { v = pack8(f); }
+};
+template <>
+struct Chunk8<float> {
+    float4 a, b;
+    __device__ void load(const float* p) {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *reinterpret_cast<const float4*>(p + 4);
+    }
+    __device__ void store(float* p) const {
+        *reinterpret_cast<float4*>(p) = a;
+        *reinterpret_cast<float4*>(p + 4) = b;
+    }
+    __device__ void get(float (&f)[8]) const {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+    __device__ void set(const float (&f)[8]) {
+        a = make_float4(f[0], f[1], f[2], f[3]);
+        b = make_float4(f[4], f[5], f[6], f[7]);
+    }
+};
+
+// A CTA takes tpc tokens x hpc heads.  The angles of its tokens are computed
+// once, in shared memory, and serve every head; then each thread takes units of
+// 8 columns (16 in the half layout's rotary part, whose pairs lie 32 columns
+// apart), kRopeUnroll of them in flight.  Bound by the bytes of x and out; the
+// small calls by the launch.
+constexpr int kRopeUnroll = 4;
+constexpr int kRopeMaxTokens = 16;
+template <typename E, bool kInterleaved>
+__global__ void __launch_bounds__(kMoveThreads) mla_rope_kernel(const __grid_constant__ RopeParams p) {
+    __shared__ float2 cs[kRopeMaxTokens][kRopePairs];
+    const int t0 = blockIdx.x * p.tpc, h0 = blockIdx.y * p.hpc;
+    const int nt = min(p.tpc, p.T - t0), nh = min(p.hpc, p.h - h0);
+    for (int i = threadIdx.x; i < nt * kRopePairs; i += kMoveThreads) {
+        const int t = i / kRopePairs, k = i % kRopePairs;
+        float2 v = rope_cos_sin(p.table.turns, p.table.amplitude, p.positions[t0 + t], k);
+        if (p.transpose) v.y = -v.y;
+        cs[t][k] = v;
+    }
+    __syncthreads();
+    constexpr int kRot = kInterleaved ? 8 : 4;  // units of the rotary part
+    const int rest = p.in_place ? 0 : (p.width - 2 * kRopePairs) / 8;
+    const int per_row = kRot + rest;
+    const int total = nt * nh * per_row;
+    const int off8 = p.offset / 8;
+    const E* x = static_cast<const E*>(p.x);
+    E* out = static_cast<E*>(p.out);
+    for (int base = threadIdx.x; base < total; base += kMoveThreads * kRopeUnroll) {
+        Chunk8<E> v[kRopeUnroll], v2[kInterleaved ? 1 : kRopeUnroll];
+        int64_t to[kRopeUnroll];
+        int unit[kRopeUnroll], tok[kRopeUnroll];
+#pragma unroll
+        for (int i = 0; i < kRopeUnroll; ++i) {
+            const int w = base + i * kMoveThreads;
+            unit[i] = -1;
+            if (w < total) {
+                const int row = w / per_row, u = w - row * per_row;
+                const int t = row / nh, hd = row - t * nh;
+                unit[i] = u;
+                tok[i] = t;
+                // rotary units first, then the columns around them
+                int c = u - kRot;
+                c = u < kRot ? off8 + u : c < off8 ? c : c + 8;
+                const E* s = x + (int64_t)(t0 + t) * p.xt + (int64_t)(h0 + hd) * p.xh + c * 8;
+                to[i] = (int64_t)(t0 + t) * p.ot + (int64_t)(h0 + hd) * p.oh + c * 8;
+                v[i].load(s);
+                if constexpr (!kInterleaved)
+                    if (u < kRot) v2[i].load(s + kRopePairs);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRopeUnroll; ++i) {
+            if (unit[i] < 0) continue;
+            if (unit[i] < kRot) {
+                const float2* c = cs[tok[i]];
+                float a[8];
+                v[i].get(a);
+                if constexpr (kInterleaved) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) rotate(a[2 * k], a[2 * k + 1], c[unit[i] * 4 + k]);
+                } else {
+                    float b[8];
+                    v2[i].get(b);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) rotate(a[k], b[k], c[unit[i] * 8 + k]);
+                    v2[i].set(b);
+                    v2[i].store(out + to[i] + kRopePairs);
+                }
+                v[i].set(a);
+            }
+            v[i].store(out + to[i]);
+        }
+    }
+    __threadfence();
+}
+
+inline bool launch_rope(const mla_rope_dims& d, const mla_rope_table& table, const void* x, const int32_t* positions, void* out,
+                        cudaStream_t stream) {
+    RopeParams p = {};
+    p.x = x;
+    p.positions = positions;
+    p.out = out;
+    p.xt = d.x_token_stride;
+    p.xh = d.x_head_stride;
+    p.ot = d.out_token_stride;
+    p.oh = d.out_head_stride;
+    p.T = d.tokens;
+    p.h = d.num_heads;
+    p.width = d.width;
+    p.offset = d.offset;
+    p.transpose = d.transpose;
+    p.in_place = x == out;
+    p.table = table;
+    // About kMoveThreads * kRopeUnroll units per CTA: several heads of a token,
+    // or several tokens where there are few heads.
+    const int per_row = (p.in_place ? 0 : (d.width - 2 * kRopePairs) / 8) + (table.interleaved ? 8 : 4);
+    const int rows = max(1, kMoveThreads * kRopeUnroll / per_row);
+    p.hpc = min(d.num_heads, rows);
+    p.tpc = min(min(kRopeMaxTokens, d.tokens), max(1, rows / p.hpc));
+    const dim3 grid((d.tokens + p.tpc - 1) / p.tpc, (d.num_heads + p.hpc - 1) / p.hpc);
+    if (grid.y > 65535) return false;
+    if (d.dtype == MLA_DTYPE_BF16) {
+        if (table.interleaved) mla_rope_kernel<__nv_bfloat16, true><<<grid, kMoveThreads, 0, stream>>>(p);
+        else mla_rope_kernel<__nv_bfloat16, false><<<grid, kMoveThreads, 0, stream>>>(p);
+    } else {
+        if (table.interleaved) mla_rope_kernel<float, true><<<grid, kMoveThreads, 0, stream>>>(p);
+        else mla_rope_kernel<float, false><<<grid, kMoveThreads, 0, stream>>>(p);
+    }
+    return true;
+}
+
+// ------------------------------------------------------------------ pool and books
+struct CachePool {
+    uint8_t* kv;
+    float* scales;  // e4m3 pools
+    int num_blocks;
+    int page_bytes;
+};
+struct CacheBooks {
+    int32_t* bt;
+    int32_t* lens;
+    int32_t* refs;
+    int32_t* status;
+    int batch, max_blocks, num_blocks;
+};
+__device__ __forceinline__ void raise(int32_t* status, int bit) {
+    if (status != nullptr) atomicOr(status, bit);
+}
+
+// Sums over the block, for block sizes that are multiples of 32 up to 1024:
+// the sum before this thread, and the total.  `tot` is 33 ints of shared memory.
+__device__ __forceinline__ int block_exclusive(int v, int* tot, int* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();  // an earlier call's readers are done
+    if (lane == 31) tot[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        const int own = lane < warps ? tot[lane] : 0;
+        int w = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        tot[lane] = w - own;
+        if (lane == 31) tot[32] = w;
+    }
+    __syncthreads();
+    *total = tot[32];
+    return tot[warp] + x - v;
+}
+
+// ------------------------------------------------------------------ append
+struct AppendParams {
+    const __nv_bfloat16* c_kv;
+    const __nv_bfloat16* k_pe;
+    int64_t c_stride, pe_stride;
+    const int32_t* off;
+    const int32_t* bt;
+    const int32_t* lens;
+    CachePool pool;
+    int32_t* status;
+    int batch, max_blocks, tokens, rotate;
+    mla_rope_table rope;
+};
+
+// Pages that request b's new rows touch; 0, with *bad set, where they do not fit.
+struct NewRows {
+    int start, L, first, pages;  // position of the first new row, length, row in c_kv, pages
+};
+__device__ __forceinline__ NewRows new_rows(const AppendParams& p, int b, bool* bad) {
+    NewRows r;
+    const int lo = p.off[b], hi = p.off[b + 1];
+    const int64_t n = (int64_t)hi - lo;
+    r.L = p.lens[b];
+    r.first = lo;
+    r.pages = 0;
+    r.start = 0;
+    if (lo < 0 || hi > p.tokens || n < 0 || n > r.L || !seqlen_in_range(r.L, p.max_blocks)) {
+        *bad = true;
+        return r;
+    }
+    r.start = r.L - (int)n;
+    if (n > 0) r.pages = pages_of(r.L) - r.start / kPage;
+    return r;
+}
+
+__device__ __forceinline__ float finite_or_nan(float x) { return fabsf(x) <= FLT_MAX ? x : __int_as_float(0x7fffffff); }
+__device__ __forceinline__ uint2 quant8(const float (&f)[8], float inv) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = e4m3x2(finite_or_nan(f[2 * e] * inv), finite_or_nan(f[2 * e + 1] * inv));
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+__device__ __forceinline__ uint32_t amax_of(uint32_t amax, float x) {
+    const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
+    return b < kInfBits ? max(amax, b) : amax;
+}
+
+// One CTA per touched page: it holds the page's new rows in registers (16 pieces of
+// 8 latent columns and 2 of 4 RoPE pairs per thread for a full page), so the scale
+// costs no second read of them.  The CTA finds its (request, page) by a scan over the
+// requests' page counts.
+template <bool kQ8>
+__global__ void __launch_bounds__(kMoveThreads) mla_cache_append_kernel(const __grid_constant__ AppendParams p) {
+    __shared__ int tot[33];
+    __shared__ int job[4];  // request, page within its new pages
+    __shared__ uint32_t warp_max[kMoveThreads / 32];
+    const int tid = threadIdx.x;
+    if (tid == 0) job[0] = -1;
+    int before = 0;
+    for (int base = 0; base < p.batch; base += kMoveThreads) {
+        const int b = base + tid;
+        bool bad = false;
+        int pages = 0;
+        if (b < p.batch) pages = new_rows(p, b, &bad).pages;
+        if (bad) raise(p.status, MLA_STATUS_BAD_ROW);
+        int total;
+        const int mine = before + block_exclusive(pages, tot, &total);
+        if ((int)blockIdx.x >= mine && (int)blockIdx.x < mine + pages) {
+            job[0] = b;
+            job[1] = blockIdx.x - mine;
+        }
+        before += total;
+        // (CTA 0 looks at every request, for the status)
+        if (blockIdx.x != 0 && (int)blockIdx.x < before) break;
+    }
+    __syncthreads();
+    const int b = job[0];
+    if (b < 0) return;
+    bool bad = false;
+    const NewRows nr = new_rows(p, b, &bad);
+    const int page = nr.start / kPage + job[1];
+    const int phys = p.bt[(size_t)b * p.max_blocks + page];
+    if ((unsigned)phys >= (unsigned)p.pool.num_blocks) {
+        if (tid == 0) raise(p.status, MLA_STATUS_BAD_BLOCK_TABLE);
+        return;
+    }
+    const int r0 = max(nr.start - page * kPage, 0), r1 = min(nr.L - page * kPage, kPage);
+    const int64_t src0 = (int64_t)nr.first + (page * kPage - nr.start);  // source row of page row 0
+    uint8_t* dst = p.pool.kv + (size_t)phys * p.pool.page_bytes;
+
+    // latent: piece tid % 64 of rows r0 + tid / 64 + 4 k;  RoPE: unit tid % 8 of rows r0 + tid / 8 + 32 k
+    const int lc = tid & 63, lr = tid >> 6, pu = tid & 7, pr = tid >> 3;
+    uint4 lat[16];
+    float pe[2][8];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const int r = r0 + lr + 4 * k;
+        if (r < r1) lat[k] = *reinterpret_cast<const uint4*>(p.c_kv + (src0 + r) * p.c_stride + lc * 8);
+    }
+    const bool inter = !p.rotate || p.rope.interleaved;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int r = r0 + pr + 32 * k;
+        if (r >= r1) continue;
+        const __nv_bfloat16* s = p.k_pe + (src0 + r) * p.pe_stride;
+        uint4 raw;
+        if (inter) {
+            raw = *reinterpret_cast<const uint4*>(s + pu * 8);
+        } else {  // pairs 4 pu .. 4 pu + 3: columns c and c + 32
+            const uint2 lo = *reinterpret_cast<const uint2*>(s + pu * 4);
+            const uint2 hi = *reinterpret_cast<const uint2*>(s + kRopePairs + pu * 4);
+            raw = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        }
+        unpack8(raw, pe[k]);
+        if (p.rotate) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 c = rope_cos_sin(p.rope.turns, p.rope.amplitude, page * kPage + r, pu * 4 + i);
+                // (selected, not indexed: both layouts keep the values in registers)
+                float a = inter ? pe[k][2 * i] : pe[k][i], z = inter ? pe[k][2 * i + 1] : pe[k][i + 4];
+                rotate(a, z, c);
+                if (inter) {
+                    pe[k][2 * i] = a;
+                    pe[k][2 * i + 1] = z;
+                } else {
+                    pe[k][i] = a;
+                    pe[k][i + 4] = z;
+                }
+            }
+        }
+    }
+    float inv = 1.f;
+    if constexpr (kQ8) {
+        uint32_t amax = 0;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            if (r0 + lr + 4 * k >= r1) continue;
+            float f[8];
+            unpack8(lat[k], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = amax_of(amax, f[i]);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (r0 + pr + 32 * k >= r1) continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = amax_of(amax, pe[k][i]);
+        }
+        amax = __reduce_max_sync(0xffffffffu, amax);
+        if ((tid & 31) == 0) warp_max[tid >> 5] = amax;
+        const float held = r0 > 0 ? p.pool.scales[phys] : 0.f;  // (read by all before thread 0 writes it)
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kMoveThreads / 32; ++w) amax = max(amax, warp_max[w]);
+        const int e = amax == 0 ? kMinScaleExp : min(max(e4m3_scale_exp(amax), kMinScaleExp), kMaxScaleExp);
+        const float scale = fmaxf(pow2f(e), held);
+        inv = 1.f / scale;
+        if (r0 > 0 && scale > held) {
+            // The page's earlier rows move to the larger scale.
+            const float f = held / scale;
+            uint2* rows = reinterpret_cast<uint2*>(dst);
+            for (int i = tid; i < r0 * (kDqk / 8); i += kMoveThreads) {
+                const uint2 v = rows[i];
+                const uint32_t w[4] = {v.x & 0xffffu, v.x >> 16, v.y & 0xffffu, v.y >> 16};
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 h = __half22float2(as_h2(h2_of_e4m3x2(w[k])));
+                    o[k] = e4m3x2(h.x * f, h.y * f);
+                }
+                rows[i] = make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
+            }
+        }
+        if (tid == 0) p.pool.scales[phys] = scale;
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const int r = r0 + lr + 4 * k;
+        if (r >= r1) continue;
+        if constexpr (kQ8) {
+            float f[8];
+            unpack8(lat[k], f);
+            *reinterpret_cast<uint2*>(dst + r * kDqk + lc * 8) = quant8(f, inv);
+        } else {
+            *reinterpret_cast<uint4*>(dst + (r * kDqk + lc * 8) * 2) = lat[k];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int r = r0 + pr + 32 * k;
+        if (r >= r1) continue;
+        if constexpr (kQ8) {
+            const uint2 v = quant8(pe[k], inv);
+            uint8_t* d = dst + r * kDqk + kDv;
+            if (inter) {
+                *reinterpret_cast<uint2*>(d + pu * 8) = v;
+            } else {
+                *reinterpret_cast<uint32_t*>(d + pu * 4) = v.x;
+                *reinterpret_cast<uint32_t*>(d + kRopePairs + pu * 4) = v.y;
+            }
+        } else {
+            const uint4 v = pack8(pe[k]);
+            __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(dst) + r * kDqk + kDv;
+            if (inter) {
+                *reinterpret_cast<uint4*>(d + pu * 8) = v;
+            } else {
+                *reinterpret_cast<uint2*>(d + pu * 4) = make_uint2(v.x, v.y);
+                *reinterpret_cast<uint2*>(d + kRopePairs + pu * 4) = make_uint2(v.z, v.w);
+            }
+        }
+    }
+    __threadfence();
+}
+
+inline void launch_append(const AppendParams& p, cudaStream_t stream) {
+    // n new rows touch at most n pages, and at most n / 64 + 2
+    const int64_t most = min((int64_t)p.tokens, (int64_t)p.tokens / kPage + 2 * (int64_t)p.batch);
+    if (p.pool.scales != nullptr) mla_cache_append_kernel<true><<<(unsigned)most, kMoveThreads, 0, stream>>>(p);
+    else mla_cache_append_kernel<false><<<(unsigned)most, kMoveThreads, 0, stream>>>(p);
+}
+
+// ------------------------------------------------------------------ page moves
+constexpr int kSliceBytes = 2 * kMoveThreads * 16;  // of a page, per CTA: two loads in flight per thread
+inline int page_slices(int page_bytes) { return (page_bytes + kSliceBytes - 1) / kSliceBytes; }
+
+__device__ __forceinline__ void copy_slice(const CachePool& pool, int src, int dst, int slice) {
+    const uint8_t* s = pool.kv + (size_t)src * pool.page_bytes;
+    uint8_t* d = pool.kv + (size_t)dst * pool.page_bytes;
+    const int a = slice * kSliceBytes + threadIdx.x * 16, b = a + kMoveThreads * 16;
+    uint4 va, vb;
+    if (a < pool.page_bytes) va = *reinterpret_cast<const uint4*>(s + a);
+    if (b < pool.page_bytes) vb = *reinterpret_cast<const uint4*>(s + b);
+    if (a < pool.page_bytes) *reinterpret_cast<uint4*>(d + a) = va;
+    if (b < pool.page_bytes) *reinterpret_cast<uint4*>(d + b) = vb;
+    if (slice == 0 && threadIdx.x == 0 && pool.scales != nullptr) pool.scales[dst] = pool.scales[src];
+}
+
+__global__ void __launch_bounds__(kMoveThreads)
+    mla_cache_copy_kernel(const CachePool pool, const int32_t* src, const int32_t* dst, int32_t* status) {
+    const int s = src[blockIdx.x], d = dst[blockIdx.x];
+    if (s < 0) return;
+    if (s >= pool.num_blocks || (unsigned)d >= (unsigned)pool.num_blocks) {
+        if (threadIdx.x == 0) raise(status, MLA_STATUS_BAD_BLOCK_TABLE);
+        return;
+    }
+    copy_slice(pool, s, d, blockIdx.y);
+    __threadfence();
+}
+inline void launch_copy_pages(const CachePool& pool, int n, const int32_t* src, const int32_t* dst, int32_t* status,
+                              cudaStream_t stream) {
+    mla_cache_copy_kernel<<<dim3(n, page_slices(pool.page_bytes)), kMoveThreads, 0, stream>>>(pool, src, dst, status);
+}
+
+// ------------------------------------------------------------------ fork
+constexpr int kForkMax = 1024;
+constexpr int kBookThreads = 1024;
+constexpr int kBookUnroll = 4;
+// workspace words of fork i
+enum ForkWord { kForkOk = 0, kForkSrc = 1, kForkDst = 2, kForkWords = 3 };
+__host__ __device__ inline size_t fork_workspace_words(int n) { return (size_t)kForkWords * n; }
+
+// One CTA decides every fork, in order: checks the rows, ranks the forks that need
+// a page and hands them the lowest free ones.
+__global__ void __launch_bounds__(kBookThreads)
+    mla_cache_fork_plan_kernel(const CacheBooks k, int n, const int32_t* parents, const int32_t* children, int32_t* ws) {
+    __shared__ int child_s[kForkMax];
+    __shared__ int fresh[kForkMax];
+    __shared__ int tot[33];
+    const int i = threadIdx.x;
+    const int parent = i < n ? parents[i] : -1, child = i < n ? children[i] : -1;
+    if (i < n) child_s[i] = child;
+    __syncthreads();
+    bool ok = i < n && (unsigned)parent < (unsigned)k.batch && (unsigned)child < (unsigned)k.batch;
+    if (ok)
+        for (int j = 0; j < i; ++j) ok &= child_s[j] != child;
+    int L = 0;
+    if (ok) {
+        L = k.lens[parent];
+        ok = seqlen_in_range(L, k.max_blocks) && k.lens[child] == 0;
+    }
+    if (i < n && !ok) raise(k.status, MLA_STATUS_BAD_ROW);
+    const int last = L / kPage;
+    int src = -1;
+    if (ok && L % kPage != 0) {
+        src = k.bt[(size_t)parent * k.max_blocks + last];
+        if ((unsigned)src >= (unsigned)k.num_blocks) {
+            raise(k.status, MLA_STATUS_BAD_BLOCK_TABLE);
+            ok = false;
+            src = -1;
+        }
+    }
+    int need;
+    const int rank = block_exclusive(src >= 0 ? 1 : 0, tot, &need);
+    // the lowest `need` free pages
+    int found = 0;
+    for (int base = 0; base < k.num_blocks && found < need; base += kBookThreads * kBookUnroll) {
+        // thread t takes kBookUnroll consecutive pages, so that ranks rise with pages
+        int at[kBookUnroll], cnt = 0;
+#pragma unroll
+        for (int u = 0; u < kBookUnroll; ++u) {
+            const int page = base + i * kBookUnroll + u;
+            at[u] = page < k.num_blocks && k.refs[page] == 0 ? 1 : 0;
+            cnt += at[u];
+        }
+        int total;
+        int r = found + block_exclusive(cnt, tot, &total);
+#pragma unroll
+        for (int u = 0; u < kBookUnroll; ++u) {
+            if (at[u] && r < need) fresh[r] = base + i * kBookUnroll + u;
+            r += at[u];
+        }
+        found += total;
+    }
+    __syncthreads();
+    int dst = -1;
+    if (src >= 0) {
+        if (rank < found) {
+            dst = fresh[rank];
+        } else {
+            raise(k.status, MLA_STATUS_NO_FREE_PAGE);
+            ok = false;
+        }
+    }
+    if (i < n) {
+        ws[kForkWords * i + kForkOk] = ok ? 1 : 0;
+        ws[kForkWords * i + kForkSrc] = ok ? src : -1;
+        ws[kForkWords * i + kForkDst] = dst;
+        if (ok && L > 0) {
+            k.lens[child] = L;
+            if (dst >= 0) {
+                k.bt[(size_t)child * k.max_blocks + last] = dst;
+                k.refs[dst] = 1;
+            }
+        }
+    }
+}
+
+// CTA (i, s): slice s of fork i's page, or (the last s) its table row.
+__global__ void __launch_bounds__(kMoveThreads)
+    mla_cache_fork_kernel(const CacheBooks k, const CachePool pool, const int32_t* parents, const int32_t* children,
+                          const int32_t* ws) {
+    const int32_t* w = ws + kForkWords * blockIdx.x;
+    if (!w[kForkOk]) return;
+    if (blockIdx.y + 1 < gridDim.y) {
+        if (w[kForkSrc] >= 0) copy_slice(pool, w[kForkSrc], w[kForkDst], blockIdx.y);
+    } else {
+        const int parent = parents[blockIdx.x], child = children[blockIdx.x];
+        const int full = k.lens[child] / kPage;
+        for (int j = threadIdx.x; j < full; j += kMoveThreads) {
+            const int page = k.bt[(size_t)parent * k.max_blocks + j];
+            k.bt[(size_t)child * k.max_blocks + j] = page;
+            if ((unsigned)page >= (unsigned)k.num_blocks) raise(k.status, MLA_STATUS_BAD_BLOCK_TABLE);
+            else atomicAdd(k.refs + page, 1);
+        }
+    }
+    __threadfence();
+}
+inline void launch_fork(const CacheBooks& k, const CachePool& pool, int n, const int32_t* parents, const int32_t* children,
+                        int32_t* ws, cudaStream_t stream) {
+    mla_cache_fork_plan_kernel<<<1, kBookThreads, 0, stream>>>(k, n, parents, children, ws);
+    mla_cache_fork_kernel<<<dim3(n, page_slices(pool.page_bytes) + 1), kMoveThreads, 0, stream>>>(k, pool, parents, children, ws);
+}
+
+// ------------------------------------------------------------------ free
+__global__ void __launch_bounds__(kMoveThreads) mla_cache_free_kernel(const CacheBooks k, const int32_t* rows) {
+    __shared__ int len;
+    const int row = rows[blockIdx.x];
+    if ((unsigned)row >= (unsigned)k.batch) {
+        if (threadIdx.x == 0) raise(k.status, MLA_STATUS_BAD_ROW);
+        return;
+    }
+    if (threadIdx.x == 0) len = atomicExch(k.lens + row, 0);  // a row named twice is empty the second time
+    __syncthreads();
+    if (!seqlen_in_range(len, k.max_blocks) && threadIdx.x == 0) raise(k.status, MLA_STATUS_BAD_SEQLEN);
+    const int pages = pages_of(clamp_seqlen(len, k.max_blocks));
+    int32_t* bt = k.bt + (size_t)row * k.max_blocks;
+    for (int j = threadIdx.x; j < pages; j += kMoveThreads) {
+        const int page = bt[j];
+        bt[j] = -1;
+        if ((unsigned)page >= (unsigned)k.num_blocks) {
+            raise(k.status, MLA_STATUS_BAD_BLOCK_TABLE);
+        } else if (atomicSub(k.refs + page, 1) <= 0) {
+            atomicAdd(k.refs + page, 1);
+            raise(k.status, MLA_STATUS_BAD_REF_COUNT);
+        }
+    }
+    __threadfence();
+}
+inline void launch_free(const CacheBooks& k, int n, const int32_t* rows, cudaStream_t stream) {
+    mla_cache_free_kernel<<<n, kMoveThreads, 0, stream>>>(k, rows);
+}
+
+// ------------------------------------------------------------------ compact
+// workspace: live, moves, then the destinations (free pages before `live`, rising)
+// and the sources (pages in use behind it, rising) one after the other, then for
+// each page behind `live` its place in that list (-1: not in use).
+enum CompactWord { kCompactLive = 0, kCompactMoves = 1, kCompactList = 4 };
+inline size_t compact_workspace_words(int num_blocks) { return kCompactList + 2 * (size_t)num_blocks; }
+
+// As many free pages lie before `live` as pages in use behind it (live counts
+// both those in use before it and those behind), so one running count over the
+// pages that move or are moved to numbers both lists.
+__global__ void __launch_bounds__(kBookThreads) mla_cache_compact_plan_kernel(const CacheBooks k, int32_t* ws) {
+    __shared__ int tot[33];
+    const int nb = k.num_blocks, i = threadIdx.x;
+    int mine = 0;
+    for (int page = i; page < nb; page += kBookThreads) mine += k.refs[page] > 0;
+    int live;
+    block_exclusive(mine, tot, &live);
+    int32_t* list = ws + kCompactList;
+    int32_t* place = list + nb;
+    int before = 0;
+    for (int base = 0; base < nb; base += kBookThreads * kBookUnroll) {
+        int at[kBookUnroll], cnt = 0;
+#pragma unroll
+        for (int u = 0; u < kBookUnroll; ++u) {
+            const int page = base + i * kBookUnroll + u;
+            at[u] = page < nb && (k.refs[page] > 0) == (page >= live) ? 1 : 0;
+            cnt += at[u];
+        }
+        int total;
+        int r = before + block_exclusive(cnt, tot, &total);
+#pragma unroll
+        for (int u = 0; u < kBookUnroll; ++u) {
+            const int page = base + i * kBookUnroll + u;
+            if (at[u]) list[r] = page;
+            if (page < nb && page >= live) place[page] = at[u] ? r : -1;
+            r += at[u];
+        }
+        before += total;
+    }
+    if (i == 0) {
+        ws[kCompactLive] = live;
+        ws[kCompactMoves] = before / 2;
+    }
+}
+
+__global__ void __launch_bounds__(kMoveThreads)
+    mla_cache_compact_kernel(const CacheBooks k, const CachePool pool, const int32_t* ws, int slices) {
+    const int live = ws[kCompactLive], moves = ws[kCompactMoves];
+    const int32_t* list = ws + kCompactList;
+    const int32_t* place = list + k.num_blocks;
+    const int64_t units = (int64_t)moves * slices;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int m = (int)(u / slices), s = (int)(u - (int64_t)m * slices);
+        const int dst = list[m], src = list[moves + m];
+        copy_slice(pool, src, dst, s);
+        if (s == 0 && threadIdx.x == 0) {
+            k.refs[dst] = k.refs[src];
+            k.refs[src] = 0;
+        }
+    }
+    for (int b = blockIdx.x; b < k.batch; b += gridDim.x) {
+        const int pages = pages_of(clamp_seqlen(k.lens[b], k.max_blocks));
+        int32_t* bt = k.bt + (size_t)b * k.max_blocks;
+        for (int j = threadIdx.x; j < pages; j += kMoveThreads) {
+            const int page = bt[j];
+            if ((unsigned)page >= (unsigned)k.num_blocks) {
+                raise(k.status, MLA_STATUS_BAD_BLOCK_TABLE);
+            } else if (page >= live) {
+                const int at = place[page];
+                if (at >= moves) bt[j] = list[at - moves];
+                else raise(k.status, MLA_STATUS_BAD_REF_COUNT);
+            }
+        }
+    }
+    __threadfence();
+}
+inline void launch_compact(const CacheBooks& k, const CachePool& pool, int32_t* ws, cudaStream_t stream) {
+    const int slices = page_slices(pool.page_bytes);
+    mla_cache_compact_plan_kernel<<<1, kBookThreads, 0, stream>>>(k, ws);
+    const int64_t most = max((int64_t)k.batch, (int64_t)(k.num_blocks / 2) * slices);
+    mla_cache_compact_kernel<<<(unsigned)min((int64_t)148 * 16, max(most, (int64_t)1)), kMoveThreads, 0, stream>>>(k, pool, ws, slices);
+}
+
+}  // namespace mla

@@ -11,8 +11,11 @@
 
 #include "absorb_kernels.cuh"
 #include "decode_kernels.cuh"
+#include "cache_kernels.cuh"
 #include "pair_kernels.cuh"
+#include "q8_kernels.cuh"
 #include "rank_combine.cuh"
+#include "mla_cache.h"
 #include "mla_decode.h"
 #include "schedule.cuh"
 
@@ -922,3 +925,6 @@ int mla_decode_combine_ranks_f32(int32_t num_ranks, int32_t batch, int32_t s_q, 
 }
 
 }  // extern "C"
+
+// The cache's operators and decode over an 8-bit cache (include/mla_cache.h).
+#include "cache_api.cuh"

@@ -1,0 +1,817 @@
+// Absorbed-MQA decode over a latent cache held in 8 bits (e4m3) with one fp32
+// scale per page of 64 tokens (and per KV head; the latent cache has one):
+//
+//   row_t = scale[page(t)] * e4m3 row t            (576 values, 576 bytes)
+//   z_t   = softmax_scale * <q, row_t>,  out = sum_t softmax(z)_t row_t[0:512]
+//
+// in the transposed order of decode_kernels.cuh: S^T = K Q^T, softmax along the
+// KV axis, O^T = V^T P^T.  Both products run as tcgen05 kind::f8f6f4 straight
+// on the cache's bytes; nothing is widened on the way.
+//
+// The other operands lose nothing to 8 bits either, because in the transposed
+// order the query columns are the MMA's N, and an MMA of N <= 64 occupies the
+// tensor pipe as long as one of N = 16.  So Q and P enter as sums of e4m3
+// terms, the terms side by side as further columns:
+//   - Q.  A bf16 value has 8 significant bits, an e4m3 value 4.  With x scaled by a
+//     power of two per query row (its largest magnitude then lies in (224, 448]),
+//     hi = e4m3(x) leaves a remainder of at most 4 significant bits, which
+//     lo = e4m3(16 (x - hi)) holds exactly.  Only values below 2^-14 of the
+//     row's largest are rounded, by at most 2^-22 of it.  S^T = S_hi + S_lo / 16.
+//   - P.  x = 16 p s / R (s the page's scale, R the largest scale so far) is rounded
+//     to fp16 (11 bits, half a step is 2^-12 of the weight: an eighth of the
+//     rounding of a bf16 result) and cut into three e4m3 terms, each 16 times the
+//     remainder of the one before, which hold those 11 bits exactly; values below
+//     2^-6 lose at most 2^-18 absolutely, 2^-22 of the largest weight.
+//     O^T = (O_0 + O_1 / 16 + O_2 / 256) R / 16.
+// The page's scale s is a factor of the score of its tokens and of their value
+// rows, so it enters the exponent of P and costs no pass over the data.
+//
+// Work split.  A step is 128 tokens (two pages; M = 128 in GEMM1), cut into four
+// boxes of 128 latent columns (16 KB each, 128-byte swizzle) and the 64 RoPE
+// columns (8 KB).  Box c is both K columns [128 c, 128 c + 128) of GEMM1 and the
+// d_v chunk c of GEMM2 (read MN-major), so the ring that holds the boxes frees
+// each one as soon as its chunk's GEMM2 is done.  The plan, the walk over work
+// items, the partial slots and the combine are those of decode_kernels.cuh
+// (64-token units).  Query groups are 16 or 32 columns; more query columns are
+// several groups that walk each range of pages side by side, one CTA per group,
+// so that all but the first read of a page hit L2.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "cache_kernels.cuh"
+#include "decode_kernels.cuh"
+
+namespace mla {
+
+constexpr int kQ8Row = kDqk;                    // bytes per token
+constexpr int kQ8PageBytes = kPage * kQ8Row;    // 36,864
+constexpr int kQ8Step = 2 * kPage;              // tokens per step
+constexpr int kQ8BoxBytes = kQ8Step * 128;      // 128 tokens x 128 latent columns
+constexpr int kQ8RopeBytes = kQ8Step * 64;      // 128 tokens x 64 RoPE columns
+constexpr int kQ8Boxes = 4;
+constexpr int kQ8RopeSlots = 2;
+constexpr int kQ8Terms = 3;                     // e4m3 terms of P
+// x = 2^kQ8Bias p: the largest weight is 2^kQ8Bias, and a weight may grow
+// 2^kQ8Grow above it before O^T is rescaled; 2^(bias + grow) <= 448.
+constexpr float kQ8Bias = 4.0f;
+constexpr float kQ8Grow = 4.0f;
+constexpr float kQ8MinBias = -60.0f;
+constexpr float kQ8Unset = -1e30f;              // running max before the first visible token
+
+struct Q8Params : FwdParams {
+    const __nv_bfloat16* q;   // [B * N][576]
+    const float* kv_scales;   // [num_blocks]
+};
+
+template <int NG>
+struct Q8Cfg {
+    static constexpr int kColGroups = NG / 16;              // softmax groups of 4 warps x 16 columns
+    static constexpr int kG1 = NG == 16 ? 2 : 1;            // GEMM1 issuers = S^T accumulators
+    static constexpr int kG2 = 1;                           // GEMM2 issuers
+    static constexpr int kFirstQ = 4;                       // warps 4..7 split Q
+    static constexpr int kFirstSoftmax = 8;
+    static constexpr int kThreads = 32 * (kFirstSoftmax + 4 * kColGroups);
+    static constexpr int kQN = 2 * NG;                      // S^T columns: hi, lo
+    static constexpr int kNP = kQ8Terms * NG;               // O^T columns per d_v chunk
+    static constexpr int kSlots = NG == 16 ? 11 : 9;        // ring of 16 KB boxes
+    // shared memory
+    static constexpr int kBoxOff = 0;
+    static constexpr int kRopeOff = kBoxOff + kSlots * kQ8BoxBytes;
+    static constexpr int kQOff = kRopeOff + kQ8RopeSlots * kQ8RopeBytes;
+    static constexpr int kQBytes = kQN * kDqk;
+    static constexpr int kPOff = kQOff + kQBytes;
+    static constexpr int kPBytes = kQ8Step * kNP;
+    static constexpr int kRedOff = kPOff + 2 * kPBytes;     // float [NG][4]
+    static constexpr int kSumOff = kRedOff + NG * 16;       // float [NG][4]
+    static constexpr int kQsOff = kSumOff + NG * 16;        // float [2][NG]: row scale x softmax scale x log2 e, by item
+    static constexpr int kVoteOff = kQsOff + 2 * NG * 4;    // uint32 [2][8]
+    static constexpr int kBarOff = kVoteOff + 64;
+    static constexpr int kNumBars = 64;
+    static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+    static constexpr int kPlanMetaOff = kMiscOff + 16;
+    static constexpr int kBytes = kPlanMetaOff + (kMetaWords + 8) * 4;
+    static constexpr int kAlloc = kBytes + 1024;
+    static_assert(kAlloc <= 227 * 1024, "shared memory budget");
+    static_assert(kQOff % 1024 == 0 && kPOff % 128 == 0 && kPBytes % 128 == 0, "operand alignment");
+    // the plan's scratch: slots past the first step's boxes
+    static constexpr int kInlinePlanMaxBG = (kSlots - kQ8Boxes) * kQ8BoxBytes / 4 - 48;
+    // TMEM columns
+    static constexpr int kSCol = 0;
+    static constexpr int kOCol = 2 * kG1 * kQN;
+    static constexpr int kTmemUsed = kOCol + kQ8Boxes * kNP;
+    static_assert(kTmemUsed <= 512, "TMEM budget");
+    static constexpr int kTmemCols = 512;
+};
+
+constexpr int kQ8MaxSlots = 11;
+enum Q8Bar {
+    kQbQFull = 0, kQbQEmpty, kQbSFull0, kQbSFull1, kQbSEmpty0, kQbSEmpty1, kQbPFull0, kQbPFull1, kQbPEmpty0, kQbPEmpty1,
+    kQbOEmpty, kQbDone1, kQbDone2, kQbQSeen,
+    kQbVote0,                            // [2 parities][2 column groups]
+    kQbMax0 = kQbVote0 + 4,              // [2 column groups]
+    kQbSum0 = kQbMax0 + 2,               // [2 column groups]
+    kQbRopeFull0 = kQbSum0 + 2,
+    kQbRopeEmpty0 = kQbRopeFull0 + kQ8RopeSlots,
+    kQbFull0 = kQbRopeEmpty0 + kQ8RopeSlots,
+    kQbEmpty0 = kQbFull0 + kQ8MaxSlots,
+    kQbCount = kQbEmpty0 + kQ8MaxSlots
+};
+static_assert(kQbCount <= Q8Cfg<16>::kNumBars, "barrier slots");
+
+// ------------------------------------------------------------------ PTX
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor of kind::f8f6f4 with e4m3 A/B and fp32 D.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, int a_mn, int b_mn) {
+    return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t e4m3x2_h2(uint32_t h2) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+    return r;
+}
+
+// Reduces 16 values over the 32 lanes of a warp; lane l returns value l / 2.
+template <bool kMax>
+__device__ __forceinline__ float reduce16(float (&v)[16], int lane) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const int off = 16 >> s, h = 8 >> s;
+        const bool upper = (lane & off) != 0;
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+            const float send = upper ? v[i] : v[i + h];
+            const float keep = upper ? v[i + h] : v[i];
+            const float got = __shfl_xor_sync(kFullMask, send, off);
+            v[i] = kMax ? fmaxf(keep, got) : keep + got;
+        }
+    }
+    const float got = __shfl_xor_sync(kFullMask, v[0], 1);
+    return kMax ? fmaxf(v[0], got) : v[0] + got;
+}
+
+// ------------------------------------------------------------------ producer
+// Physical page of logical page j; a bad entry is reported and read as page 0.
+__device__ __forceinline__ int q8_page(const Q8Params& p, const Item& item, int j) {
+    int phys = __ldg(p.block_table + (size_t)item.b * p.max_blocks + j);
+    if ((unsigned)phys >= (unsigned)p.num_blocks) {
+        atomicOr(p.status, MLA_STATUS_BAD_BLOCK_TABLE);
+        phys = 0;
+    }
+    return phys;
+}
+
+// Loads box c (< 4: latent columns, 4: RoPE) of a step of one or two pages.
+__device__ __forceinline__ void q8_load(const CUtensorMap* kv_map, const CUtensorMap* rope_map, uint32_t dst, uint32_t bar,
+                                        int c, int ph0, int ph1, uint64_t policy) {
+    const bool rope = c == kQ8Boxes;
+    const uint32_t half = rope ? kQ8RopeBytes / 2 : kQ8BoxBytes / 2;
+    mbar_arrive_expect_tx(bar, ph1 >= 0 ? 2 * half : half);
+    const CUtensorMap* map = rope ? rope_map : kv_map;
+    tma_load_3d_hint(dst, map, bar, 128 * c, 0, ph0, policy);
+    if (ph1 >= 0) tma_load_3d_hint(dst + half, map, bar, 128 * c, 0, ph1, policy);
+}
+
+template <int NG>
+__device__ void q8_producer(const CUtensorMap* kv_map, const CUtensorMap* rope_map, const Q8Params& p, const int32_t* meta,
+                            uint8_t* smem, const Ctl& ctl, bool first_issued) {
+    using C = Q8Cfg<NG>;
+    const uint32_t bar0 = smem_addr(smem + C::kBarOff);
+    const uint32_t box0 = smem_addr(smem + C::kBoxOff), rope0 = smem_addr(smem + C::kRopeOff);
+    const uint64_t policy = p.share > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+    WorkIter it;
+    it.init(meta, p);
+    Item item;
+    uint32_t n = 0, r = 0;                 // boxes and RoPE boxes issued (or left out by the test hook)
+    const bool stall = p.test_stall != 0;
+    bool ok = true;
+    while (ok && it.next(p, item)) {
+        for (int j = item.p0; ok && j < item.p1; j += 2) {
+            if (r == 0 && (first_issued || stall)) {  // issued before the wait on the previous grid, or left out
+                n = kQ8Boxes;
+                r = 1;
+                continue;
+            }
+            const int ph0 = q8_page(p, item, j);
+            const int ph1 = j + 1 < item.p1 ? q8_page(p, item, j + 1) : -1;
+#pragma unroll 1
+            for (int c = 0; c < kQ8Boxes; ++c, ++n) {
+                const uint32_t slot = n % C::kSlots;
+                ok = wait_bounded(bar0 + 8 * (kQbEmpty0 + slot), ((n / C::kSlots) & 1) ^ 1, ctl);
+                if (!ok) break;
+                q8_load(kv_map, rope_map, box0 + slot * kQ8BoxBytes, bar0 + 8 * (kQbFull0 + slot), c, ph0, ph1, policy);
+            }
+            if (!ok) break;
+            const uint32_t slot = r % kQ8RopeSlots;
+            ok = wait_bounded(bar0 + 8 * (kQbRopeEmpty0 + slot), ((r / kQ8RopeSlots) & 1) ^ 1, ctl);
+            if (!ok) break;
+            q8_load(kv_map, rope_map, rope0 + slot * kQ8RopeBytes, bar0 + 8 * (kQbRopeFull0 + slot), kQ8Boxes, ph0, ph1, policy);
+            ++r;
+        }
+    }
+    if (!ok) {
+        // Let the copies already issued land before the CTA exits.
+        for (uint32_t k = 0; k < C::kSlots; ++k) {
+            const uint32_t count = n > k ? (n - k + C::kSlots - 1) / C::kSlots : 0;
+            if (count > (stall && k < kQ8Boxes ? 1u : 0u)) wait_drain(bar0 + 8 * (kQbFull0 + k), (count - 1) & 1);
+        }
+        for (uint32_t k = 0; k < kQ8RopeSlots; ++k) {
+            const uint32_t count = r > k ? (r - k + kQ8RopeSlots - 1) / kQ8RopeSlots : 0;
+            if (count > (stall && k == 0 ? 1u : 0u)) wait_drain(bar0 + 8 * (kQbRopeFull0 + k), (count - 1) & 1);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ Q split
+// Four warps cut the item's query rows into hi and lo terms while the previous
+// item's softmax and epilogue run: 8 lanes per row, 16 rows at a time.  The
+// result is GEMM1's K-major B operand without swizzle: 16-byte pieces, piece
+// (k, n) of K bytes [16 k, 16 k + 16) and column n at (k * kQN + n) * 16.
+template <int NG>
+__device__ void q8_split_q(const Q8Params& p, const int32_t* meta, uint8_t* smem, const Ctl& ctl) {
+    using C = Q8Cfg<NG>;
+    const uint32_t bar0 = smem_addr(smem + C::kBarOff);
+    const int tid = threadIdx.x - 32 * C::kFirstQ;
+    const int lane8 = tid & 7;
+    float* qs = reinterpret_cast<float*>(smem + C::kQsOff);
+    WorkIter it;
+    it.init(meta, p);
+    Item item;
+    uint32_t q_it = 0;
+    while (it.next(p, item)) {
+        bool ready = false;
+#pragma unroll 1
+        for (int pass = 0; pass < NG / 16; ++pass) {
+            const int col = pass * 16 + (tid >> 3);
+            const int gc = item.g * NG + col;
+            uint4 raw[9];
+#pragma unroll
+            for (int i = 0; i < 9; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+            if (gc < p.N) {
+                // (plain loads: a read-only load may be scheduled above the wait on the grid that wrote q)
+                const uint4* row = reinterpret_cast<const uint4*>(p.q + ((size_t)item.b * p.N + gc) * kDqk);
+#pragma unroll
+                for (int i = 0; i < 9; ++i) raw[i] = row[i * 8 + lane8];
+            }
+            uint32_t amax = 0;  // as bits of |x|: non-finite values are the largest
+#pragma unroll
+            for (int i = 0; i < 9; ++i) {
+                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    amax = max(amax, (w[e] << 16) & 0x7fffffffu);
+                    amax = max(amax, w[e] & 0x7fff0000u);
+                }
+            }
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(kFullMask, amax, o));
+            int ex = e4m3_scale_exp(amax);
+            ex = amax == 0 ? 0 : max(ex, -100);
+            // a row with an infinity or a NaN becomes NaN: so do its scores
+            const float inv = amax >= 0x7f800000u ? __int_as_float(0x7fffffff) : pow2f(-ex);
+            if (!ready) {
+                // GEMM1 of the previous item has read its Q, and its softmax has
+                // begun (so it is past its wait on kQbQFull, and done with the
+                // row scales of the item before).
+                if (!wait_warp(bar0 + 8 * kQbQEmpty, (q_it & 1) ^ 1, ctl)) return;
+                if (!wait_warp(bar0 + 8 * kQbQSeen, (q_it & 1) ^ 1, ctl)) return;
+                ready = true;
+            }
+            if (lane8 == 0)
+                qs[(q_it & 1) * NG + col] = (amax >= 0x7f800000u ? 1.f : pow2f(ex)) * p.scale_log2;
+            uint8_t* dst = smem + C::kQOff + col * 16;
+#pragma unroll
+            for (int i = 0; i < 9; ++i) {
+                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                uint32_t hi[2], lo[2];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float a = __uint_as_float(w[e] << 16) * inv, b = __uint_as_float(w[e] & 0xffff0000u) * inv;
+                    const uint32_t h = e4m3x2(a, b);
+                    const float2 back = __half22float2(as_h2(h2_of_e4m3x2(h)));
+                    const uint32_t l = e4m3x2((a - back.x) * 16.f, (b - back.y) * 16.f);
+                    if (e & 1) {
+                        hi[e >> 1] |= h << 16;
+                        lo[e >> 1] |= l << 16;
+                    } else {
+                        hi[e >> 1] = h;
+                        lo[e >> 1] = l;
+                    }
+                }
+                const int kb = (i * 8 + lane8) * 8;
+                uint8_t* d = dst + (kb >> 4) * (C::kQN * 16) + (kb & 15);
+                *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2*>(d + NG * 16) = make_uint2(lo[0], lo[1]);
+            }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar0 + 8 * kQbQFull);
+        ++q_it;
+    }
+}
+
+// ------------------------------------------------------------------ MMA issuers
+// S^T[128 x 2 NG] = K[128 x 576] . [Q_hi | Q_lo]^T.  Issuer 0 of two takes boxes
+// 0 and 1 and the RoPE box, issuer 1 boxes 2 and 3, each into its own accumulator.
+template <int NG>
+__device__ void q8_gemm1(const Q8Params& p, const int32_t* meta, uint8_t* smem, uint32_t tmem, const Ctl& ctl, int issuer) {
+    using C = Q8Cfg<NG>;
+    constexpr uint32_t kIdesc = idesc_e4m3_f32(kQ8Step, C::kQN, 0, 0);
+    const uint32_t bar0 = smem_addr(smem + C::kBarOff);
+    const uint64_t a0 = smem_desc(smem_addr(smem + C::kBoxOff), 16, 1024, kSwizzle128);
+    const uint64_t r0 = smem_desc(smem_addr(smem + C::kRopeOff), 16, 512, kSwizzle64);
+    const uint64_t b0 = smem_desc(smem_addr(smem + C::kQOff), C::kQN * 16, 128, kSwizzleNone);
+    constexpr int kPer = kQ8Boxes / C::kG1;
+    WorkIter it;
+    it.init(meta, p);
+    Item item;
+    uint32_t s_it = 0, q_it = 0;
+    bool ok = true;
+    while (ok && it.next(p, item)) {
+        ok = wait_bounded(bar0 + 8 * kQbQFull, q_it & 1, ctl);
+        if (!ok) break;
+        for (int j = item.p0; j < item.p1; j += 2) {
+            const int sb = s_it & 1;
+            ok = wait_bounded(bar0 + 8 * (kQbSEmpty0 + sb), ((s_it >> 1) & 1) ^ 1, ctl);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d = tmem + C::kSCol + (sb * C::kG1 + issuer) * C::kQN;
+            uint32_t acc = 0;
+#pragma unroll 1
+            for (int c = issuer * kPer; c < (issuer + 1) * kPer; ++c) {
+                const uint32_t n = s_it * kQ8Boxes + c, slot = n % C::kSlots;
+                ok = wait_bounded(bar0 + 8 * (kQbFull0 + slot), (n / C::kSlots) & 1, ctl);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    umma_f8(d, a0 + ((slot * kQ8BoxBytes + k * 32) >> 4), b0 + ((8 * c + 2 * k) * C::kQN), kIdesc, acc);
+                    acc = 1;
+                }
+            }
+            if (!ok) break;
+            if (issuer == 0) {
+                const uint32_t slot = s_it % kQ8RopeSlots;
+                ok = wait_bounded(bar0 + 8 * (kQbRopeFull0 + slot), (s_it / kQ8RopeSlots) & 1, ctl);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    umma_f8(d, r0 + ((slot * kQ8RopeBytes + k * 32) >> 4), b0 + ((8 * kQ8Boxes + 2 * k) * C::kQN), kIdesc, 1);
+                umma_commit(bar0 + 8 * (kQbRopeEmpty0 + slot));
+            }
+            umma_commit(bar0 + 8 * (kQbSFull0 + sb));
+            if (j + 2 >= item.p1) umma_commit(bar0 + 8 * kQbQEmpty);
+            ++s_it;
+        }
+        ++q_it;
+    }
+    umma_commit(bar0 + 8 * kQbDone1);  // drained before TMEM is released
+    wait_drain(bar0 + 8 * kQbDone1, 0);
+}
+
+// O^T chunk c [128 x 3 NG] += V^T (box c, read MN-major) . P^T (MN-major without
+// swizzle: 16-byte pieces of 16 columns, 128 tokens apart by 2 KB).
+template <int NG>
+__device__ void q8_gemm2(const Q8Params& p, const int32_t* meta, uint8_t* smem, uint32_t tmem, const Ctl& ctl, int issuer) {
+    using C = Q8Cfg<NG>;
+    constexpr uint32_t kIdesc = idesc_e4m3_f32(128, C::kNP, 1, 1);
+    const uint32_t bar0 = smem_addr(smem + C::kBarOff);
+    const uint64_t a0 = smem_desc(smem_addr(smem + C::kBoxOff), kQ8BoxBytes, 1024, kSwizzle128);
+    const uint64_t b0 = smem_desc(smem_addr(smem + C::kPOff), 128, kQ8Step * 16, kSwizzleNone);
+    constexpr int kPer = kQ8Boxes / C::kG2;
+    WorkIter it;
+    it.init(meta, p);
+    Item item;
+    uint32_t s_it = 0, item_it = 0;
+    bool ok = true;
+    while (ok && it.next(p, item)) {
+        for (int j = item.p0; j < item.p1; j += 2) {
+            const int pb = s_it & 1;
+            ok = wait_bounded(bar0 + 8 * (kQbPFull0 + pb), (s_it >> 1) & 1, ctl);
+            if (!ok) break;
+            if (j == item.p0) {
+                ok = wait_bounded(bar0 + 8 * kQbOEmpty, (item_it & 1) ^ 1, ctl);
+                if (!ok) break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int cc = 0; cc < kPer; ++cc) {
+                const int c = issuer * kPer + cc;
+                const uint32_t slot = (s_it * kQ8Boxes + c) % C::kSlots;
+#pragma unroll
+                for (int k = 0; k < kQ8Step / 32; ++k)
+                    umma_f8(tmem + C::kOCol + c * C::kNP, a0 + ((slot * kQ8BoxBytes + k * 4096) >> 4),
+                            b0 + ((pb * C::kPBytes + k * 512) >> 4), kIdesc, (j == item.p0 && k == 0) ? 0u : 1u);
+                umma_commit(bar0 + 8 * (kQbEmpty0 + slot));
+            }
+            umma_commit(bar0 + 8 * (kQbPEmpty0 + pb));
+            ++s_it;
+        }
+        if (!ok) break;
+        ++item_it;
+    }
+    umma_commit(bar0 + 8 * kQbDone2);
+    wait_drain(bar0 + 8 * kQbDone2, 0);
+}
+
+// ------------------------------------------------------------------ softmax
+// 16 weights x (fp16 range) as three e4m3 terms, stored as 16-byte pieces 2 KB
+// times the column groups apart.
+__device__ __forceinline__ void q8_store_p(const float (&x)[16], uint8_t* dst, int term_stride) {
+    uint32_t w[kQ8Terms][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+#pragma unroll
+        for (int t = 0; t < kQ8Terms; ++t) {
+            const uint32_t v = e4m3x2_h2(as_u32(h));
+            if (i & 1) w[t][i >> 1] |= v << 16;
+            else w[t][i >> 1] = v;
+            // the remainder is exact in fp16: at most 7 significant bits
+            if (t + 1 < kQ8Terms) h = __hmul2(__hsub2(h, as_h2(h2_of_e4m3x2(v))), __float2half2_rn(16.f));
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < kQ8Terms; ++t)
+        *reinterpret_cast<uint4*>(dst + t * term_stride) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+}
+
+template <int NG>
+__device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem, uint32_t tmem, const Ctl& ctl) {
+    using C = Q8Cfg<NG>;
+    const int lane = threadIdx.x & 31;
+    const int wq = (threadIdx.x >> 5) & 3;                       // TMEM lane quadrant
+    const int cg = ((threadIdx.x >> 5) - C::kFirstSoftmax) >> 2;  // columns [16 cg, 16 cg + 16)
+    const int row = 32 * wq + lane;                              // token of the step
+    const uint32_t tm = tmem + (static_cast<uint32_t>(32 * wq) << 16);
+    const uint32_t bar0 = smem_addr(smem + C::kBarOff);
+    float* red = reinterpret_cast<float*>(smem + C::kRedOff) + cg * 64;   // [16][4]: a step's maxima
+    float* sums = reinterpret_cast<float*>(smem + C::kSumOff) + cg * 64;  // [16][4]
+    const float* qs_ring = reinterpret_cast<const float*>(smem + C::kQsOff) + cg * 16;
+    uint32_t* vote = reinterpret_cast<uint32_t*>(smem + C::kVoteOff) + cg * 4;
+    constexpr int kTermStride = NG * kQ8Step;
+    uint8_t* pbase = smem + C::kPOff + cg * 16 * kQ8Step + row * 16;
+    const bool causal2 = p.causal && p.s_q > 1;
+    WorkIter it;
+    it.init(meta, p);
+    Item item;
+    uint32_t s_it = 0, item_it = 0, max_it = 0;
+    bool ok = true;
+    while (ok && it.next(p, item)) {
+        ok = wait_warp(bar0 + 8 * kQbQFull, item_it & 1, ctl);
+        if (!ok) break;
+        mbar_arrive(bar0 + 8 * kQbQSeen);
+        const float4* qs4 = reinterpret_cast<const float4*>(qs_ring + (item_it & 1) * NG);
+        const int gc0 = item.g * NG + cg * 16;  // first query column of the group
+        // scales of the item's pages, fetched a step ahead
+        auto page_scale = [&](int j) -> float {
+            if (j >= item.p1) j = item.p1 - 1;
+            const int phys = __ldg(p.block_table + (size_t)item.b * p.max_blocks + j);
+            // (a page of scale 0 holds zeros; the floor keeps its tokens' weights finite)
+            return fmaxf(__ldg(p.kv_scales + ((unsigned)phys < (unsigned)p.num_blocks ? phys : 0)), 1e-30f);
+        };
+        float sc0 = page_scale(item.p0), sc1 = page_scale(item.p0 + 1);
+        float m[16], l[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            m[c] = kQ8Unset;
+            l[c] = 0.f;
+        }
+        float R = fmaxf(sc0, sc1);
+        for (int j = item.p0; j < item.p1; j += 2) {
+            const float nx0 = page_scale(j + 2), nx1 = page_scale(j + 3);
+            const float ks = wq < 2 ? sc0 : sc1;  // this token's page
+            const int sb = s_it & 1;
+            ok = wait_warp(bar0 + 8 * (kQbSFull0 + sb), (s_it >> 1) & 1, ctl);
+            if (!ok) break;
+            tc_fence_after();
+            float z[16];
+            {
+                float lo[16];
+                const uint32_t s = tm + C::kSCol + sb * C::kG1 * C::kQN + cg * 16;
+                tmem_ld_x16(s, z);
+                tmem_ld_x16(s + NG, lo);
+                if constexpr (C::kG1 == 2) {
+                    float z2[16], lo2[16];
+                    tmem_ld_x16(s + C::kQN, z2);
+                    tmem_ld_x16(s + C::kQN + NG, lo2);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        z[c] += z2[c];
+                        lo[c] += lo2[c];
+                    }
+                } else {
+                    tmem_ld_wait();
+                }
+                tc_fence_before();
+                mbar_arrive(bar0 + 8 * (kQbSEmpty0 + sb));
+#pragma unroll
+                for (int c4 = 0; c4 < 4; ++c4) {
+                    const float4 f = qs4[c4];
+                    z[4 * c4 + 0] = fmaf(lo[4 * c4 + 0], 0.0625f, z[4 * c4 + 0]) * (f.x * ks);
+                    z[4 * c4 + 1] = fmaf(lo[4 * c4 + 1], 0.0625f, z[4 * c4 + 1]) * (f.y * ks);
+                    z[4 * c4 + 2] = fmaf(lo[4 * c4 + 2], 0.0625f, z[4 * c4 + 2]) * (f.z * ks);
+                    z[4 * c4 + 3] = fmaf(lo[4 * c4 + 3], 0.0625f, z[4 * c4 + 3]) * (f.w * ks);
+                }
+            }
+            const int t = j * kPage + row;
+            const int end = (j + 2 < item.p1 ? j + 2 : item.p1) * kPage;  // tokens of the step
+            const int lim0 = item.L - (causal2 ? 1 : 0);
+            if (end > lim0 || j + 2 > item.p1) {
+                // The step holds tokens that some column does not see (past the
+                // length, the causal rule, or no second page).
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const int lim = causal2 && gc0 + c < p.heads ? lim0 : item.L;
+                    if (t >= lim || t >= end) z[c] = -INFINITY;
+                }
+            }
+            // Does any weight exceed the running reference by more than 2^kQ8Grow?
+            bool grow = false;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) grow |= z[c] > m[c] + kQ8Grow;
+            const uint32_t gw = __any_sync(kFullMask, grow) ? 1u : 0u;
+            if (lane == 0) vote[(s_it & 1) * 8 + wq] = gw;
+            const uint32_t vbar = bar0 + 8 * (kQbVote0 + (s_it & 1) * 2 + cg);
+            mbar_arrive(vbar);
+            ok = wait_warp(vbar, (s_it >> 1) & 1, ctl);
+            if (!ok) break;
+            const uint4 v4 = *reinterpret_cast<const uint4*>(vote + (s_it & 1) * 8);
+            const float Rn = fmaxf(R, fmaxf(sc0, sc1));
+            const bool grown = (v4.x | v4.y | v4.z | v4.w) != 0;  // the same for the group's four warps
+            if (grown || Rn > R) {
+                // Move the references and rescale what is accumulated.
+                float alpha[16];
+                const float ra = R / Rn;
+                if (grown) {
+                    float zr[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) zr[c] = z[c];
+                    const float wmax = reduce16<true>(zr, lane);
+                    if ((lane & 1) == 0) red[(lane >> 1) * 4 + wq] = wmax;
+                    mbar_arrive(bar0 + 8 * (kQbMax0 + cg));
+                    ok = wait_warp(bar0 + 8 * (kQbMax0 + cg), max_it & 1, ctl);
+                    ++max_it;
+                    if (!ok) break;
+                }
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    float a = 1.f;
+                    if (grown) {
+                        const float4 r4 = *reinterpret_cast<const float4*>(red + c * 4);
+                        const float mx = fmaxf(fmaxf(r4.x, r4.y), fmaxf(r4.z, r4.w));
+                        if (mx > m[c] + kQ8Grow) {
+                            a = ex2_approx(m[c] - mx);
+                            m[c] = mx;
+                        }
+                    }
+                    l[c] *= a;
+                    alpha[c] = a * ra;
+                }
+                R = Rn;
+                if (j > item.p0) {
+                    const uint32_t prev = s_it - 1;
+                    ok = wait_warp(bar0 + 8 * (kQbPEmpty0 + (prev & 1)), (prev >> 1) & 1, ctl);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int i = 0; i < kQ8Boxes * kQ8Terms; ++i) {
+                        float o[16];
+                        const uint32_t ta = tm + C::kOCol + i * NG + cg * 16;
+                        tmem_ld_x16(ta, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) o[c] *= alpha[c];
+                        tmem_st_x16(ta, o);
+                    }
+                    tmem_st_wait();
+                }
+            }
+            const float bias = kQ8Bias + __log2f(ks / R);
+            if (bias > kQ8MinBias) {
+                const float back = exp2f(-bias);  // x -> p
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    z[c] = ex2_approx(z[c] - m[c] + bias);
+                    l[c] = fmaf(z[c], back, l[c]);
+                }
+            } else {
+                // A page whose values are next to nothing beside the largest
+                // page's still counts in full in the sum of the weights.
+                const float f = exp2f(bias);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    z[c] = ex2_approx(z[c] - m[c]);
+                    l[c] += z[c];
+                    z[c] *= f;
+                }
+            }
+            const int pb = s_it & 1;
+            ok = wait_warp(bar0 + 8 * (kQbPEmpty0 + pb), ((s_it >> 1) & 1) ^ 1, ctl);
+            if (!ok) break;
+            q8_store_p(z, pbase + pb * C::kPBytes, kTermStride);
+            if (j + 2 >= item.p1 && t >= (end < item.L ? end : item.L)) {
+                // Rows behind the sequence, or of an absent second page: their
+                // weights are zero, but what lies there (stale rows, or no row
+                // at all) may be NaN, so the row is cleared for GEMM2.
+                if (cg == 0) {
+#pragma unroll 1
+                    for (int c = 0; c < kQ8Boxes; ++c) {
+                        const uint32_t slot = (s_it * kQ8Boxes + c) % C::kSlots;
+                        uint4* d = reinterpret_cast<uint4*>(smem + C::kBoxOff + slot * kQ8BoxBytes + row * 128);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) d[i] = make_uint4(0, 0, 0, 0);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            mbar_arrive(bar0 + 8 * (kQbPFull0 + pb));
+            sc0 = nx0;
+            sc1 = nx1;
+            ++s_it;
+        }
+        if (!ok) break;
+
+        // ---- epilogue ----
+        {
+            const float wsum = reduce16<false>(l, lane);
+            if ((lane & 1) == 0) sums[(lane >> 1) * 4 + wq] = wsum;
+        }
+        mbar_arrive(bar0 + 8 * (kQbSum0 + cg));
+        ok = wait_warp(bar0 + 8 * (kQbSum0 + cg), item_it & 1, ctl);
+        if (!ok) break;
+        const uint32_t last = s_it - 1;
+        float inv[16], m_own = 0.f, l_own = 0.f;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            const float4 s4 = *reinterpret_cast<const float4*>(sums + c * 4);
+            const float ls = (s4.x + s4.y) + (s4.z + s4.w);
+            inv[c] = ls == 0.f ? 0.f : __fdividef(R * 0.0625f, ls);
+            m_own = row == c ? m[c] : m_own;
+            l_own = row == c ? ls : l_own;
+        }
+        if (row < 16 && gc0 + row < p.N) {
+            const int gc = gc0 + row;
+            const float lse = l_own == 0.f ? -INFINITY : (m_own + log2f(l_own)) * kLn2;
+            if (item.unsplit) {
+                const int sq = gc / p.heads;
+                p.lse[((size_t)item.b * p.heads + (gc - sq * p.heads)) * p.s_q + sq] = lse;
+            } else if (item.slot >= 0) {
+                // (the combine's maximum passes over a NaN; an infinity makes its
+                // weights NaN, and so the merged row)
+                p.lpart[(size_t)item.slot * NG + cg * 16 + row] = isnan(lse) ? INFINITY : lse;
+            }
+        }
+        ok = wait_warp(bar0 + 8 * (kQbPEmpty0 + (last & 1)), (last >> 1) & 1, ctl);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int ch = 0; ch < kQ8Boxes; ++ch) {
+            float o[16], o1[16], o2[16];
+            const uint32_t ta = tm + C::kOCol + ch * C::kNP + cg * 16;
+            tmem_ld_x16(ta, o);
+            tmem_ld_x16(ta + NG, o1);
+            tmem_ld_x16(ta + 2 * NG, o2);
+            tmem_ld_wait();
+            const int d = ch * 128 + row;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const float v = fmaf(fmaf(o2[c], 0.0625f, o1[c]), 0.0625f, o[c]) * inv[c];
+                if (!item.unsplit) {
+                    if (item.slot >= 0) p.opart[((size_t)item.slot * NG + cg * 16 + c) * kDv + d] = v;
+                } else if (gc0 + c < p.N) {
+                    const size_t at = ((size_t)item.b * p.N + gc0 + c) * kDv + d;
+                    if (p.out_f32) static_cast<float*>(p.out)[at] = v;
+                    else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+                }
+            }
+        }
+        if (!item.unsplit && item.slot < 0 && row == 0) atomicOr(p.status, MLA_STATUS_BAD_SCHEDULE);
+        tc_fence_before();
+        mbar_arrive(bar0 + 8 * kQbOEmpty);
+        ++item_it;
+    }
+}
+
+// ------------------------------------------------------------------ kernel
+template <int NG>
+__global__ void __launch_bounds__(Q8Cfg<NG>::kThreads, 1)
+    mla_decode_q8_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap rope_map,
+                         const Q8Params p) {
+    using C = Q8Cfg<NG>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    griddep_launch_dependents();
+    const uint32_t bar0 = smem_addr(smem + C::kBarOff);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+    int32_t* meta_s = reinterpret_cast<int32_t*>(smem + C::kPlanMetaOff);
+    constexpr int kSm = 128 * C::kColGroups;  // softmax threads
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kQbCount; ++i) {
+            uint32_t count = 1;
+            if (i == kQbSEmpty0 || i == kQbSEmpty1 || i == kQbPFull0 || i == kQbPFull1 || i == kQbOEmpty || i == kQbQSeen)
+                count = kSm;
+            if ((i >= kQbVote0 && i < kQbRopeFull0) || i == kQbQFull) count = 128;
+            if (i == kQbSFull0 || i == kQbSFull1 || i == kQbQEmpty || i == kQbDone1) count = C::kG1;
+            if (i == kQbPEmpty0 || i == kQbPEmpty1 || i == kQbDone2) count = C::kG2;
+            mbar_init(bar0 + 8 * i, count);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_addr(tmem_slot), C::kTmemCols);
+        tmem_relinquish();
+    }
+    if (p.plan_out != nullptr)
+        for (int i = 32 * threadIdx.x; i < p.BG / p.Hg; i += 32 * blockDim.x) prefetch_l2_line(p.seqlens + i);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // The plan from the lengths, and the first step's pages, before the wait on
+    // the grid before this one (see mla_decode_fwd_kernel).
+    int32_t* plan_scratch = reinterpret_cast<int32_t*>(smem + C::kBoxOff + kQ8Boxes * kQ8BoxBytes);
+    bool first_issued = false;
+    if (p.plan_out != nullptr) {
+        build_plan_in_cta(p, plan_scratch, meta_s);
+        if (threadIdx.x == 0 && p.test_stall == 0) {
+            WorkIter it;
+            it.init(meta_s, p);
+            Item item;
+            if (it.next(p, item)) {
+                const int32_t* bt = p.block_table + (size_t)item.b * p.max_blocks + item.p0;
+                const int ph0 = __ldg(bt), ph1 = item.p0 + 1 < item.p1 ? __ldg(bt + 1) : -1;
+                // (a bad entry is left to the producer, which reports it after the wait)
+                if ((unsigned)ph0 < (unsigned)p.num_blocks &&
+                    (item.p0 + 1 >= item.p1 || (unsigned)ph1 < (unsigned)p.num_blocks)) {
+                    const uint64_t policy = p.share > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+                    for (int c = 0; c < kQ8Boxes; ++c)
+                        q8_load(&kv_map, &rope_map, smem_addr(smem + C::kBoxOff) + c * kQ8BoxBytes, bar0 + 8 * (kQbFull0 + c),
+                                c, ph0, ph1, policy);
+                    q8_load(&kv_map, &rope_map, smem_addr(smem + C::kRopeOff), bar0 + 8 * kQbRopeFull0, kQ8Boxes, ph0, ph1,
+                            policy);
+                    first_issued = true;
+                }
+            }
+        }
+    }
+    griddep_wait();
+    const uint32_t tmem = *tmem_slot;
+    const int32_t* meta;
+    if (p.plan_out != nullptr) {
+        fence_proxy_async_smem();  // the scratch, before copies land there
+        publish_plan_in_cta(p, NG, plan_scratch, meta_s);
+        meta = meta_s;
+    } else {
+        const int32_t* hdr = p.sched;
+        if (hdr[kHdrMagic] != kSchedMagic || hdr[kHdrG] != p.G || hdr[kHdrBG] != p.BG || hdr[kHdrHg] != p.Hg ||
+            hdr[kHdrNG] != NG || hdr[kHdrShift] != kPageShift || hdr[kHdrShareHg] != p.share) {
+            if (threadIdx.x == 0) atomicOr(p.status, MLA_STATUS_BAD_SCHEDULE);
+            if (warp == 1) {
+                tc_fence_after();
+                tmem_dealloc(tmem, C::kTmemCols);
+            }
+            return;
+        }
+        meta = hdr + kHdrWords + (size_t)(blockIdx.x / p.share) * kMetaWords;
+    }
+    const Ctl ctl{abort_flag, p.status};
+    if (warp == 0) {
+        if (lane == 0) q8_producer<NG>(&kv_map, &rope_map, p, meta, smem, ctl, first_issued);
+    } else if (warp <= C::kG1) {
+        if (lane == 0) q8_gemm1<NG>(p, meta, smem, tmem, ctl, warp - 1);
+    } else if (warp == 3) {
+        if (lane == 0) q8_gemm2<NG>(p, meta, smem, tmem, ctl, 0);
+    } else if (warp >= C::kFirstSoftmax) {
+        q8_softmax<NG>(p, meta, smem, tmem, ctl);
+    } else if (warp >= C::kFirstQ) {
+        q8_split_q<NG>(p, meta, smem, ctl);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+}  // namespace mla

@@ -1,0 +1,226 @@
+"""Fork, free, copy and compaction of pages against the oracle's plain loops: books and
+pages are equal to the last bit."""
+import numpy as np
+import pytest
+import torch
+
+from mla_decode_attention_15_b200 import _build, binding as bd, cache as ca
+from oracle import cache as oc
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    _build.build()
+    return torch.device("cuda:0")
+
+
+class World:
+    """A pool and its books, on the GPU and as the oracle's numpy copy."""
+
+    def __init__(self, lens, nb, dev, q8=True, rows=None, width=None, seed=0):
+        g = torch.Generator().manual_seed(seed)
+        rows = rows or len(lens)
+        width = width or max(oc.pages_of(n) for n in lens) + 1
+        ids = torch.randperm(nb, generator=g).int()
+        bt = torch.full((rows, width), -7, dtype=torch.int32)  # unused entries are nobody's
+        k = 0
+        for b, n in enumerate(lens):
+            bt[b, :oc.pages_of(n)] = ids[k:k + oc.pages_of(n)]
+            k += oc.pages_of(n)
+        assert k <= nb
+        full = torch.zeros(rows, dtype=torch.int32)
+        full[:len(lens)] = torch.tensor(lens, dtype=torch.int32)
+        refs = torch.zeros(nb, dtype=torch.int32)
+        refs[ids[:k].long()] = 1
+        pool = torch.randint(0, 256, (nb, 64, 1, 576 * (1 if q8 else 2)), generator=g, dtype=torch.uint8)
+        self.scales = torch.randn(nb, 1, generator=g) if q8 else None
+        self.np = dict(bt=bt.numpy().copy(), lens=full.numpy().copy(), refs=refs.numpy().copy(), pool=pool.numpy().copy(),
+                       scales=self.scales.numpy().copy() if q8 else None)
+        self.bt, self.lens, self.refs = bt.to(dev), full.to(dev), refs.to(dev)
+        self.pool = pool.to(dev).view(torch.float8_e4m3fn if q8 else torch.bfloat16)
+        self.scales = self.scales.to(dev) if q8 else None
+        self.status, self.dev = torch.zeros(1, dtype=torch.int32, device=dev), dev
+
+    def t(self, v):
+        return torch.tensor(v, dtype=torch.int32, device=self.dev)
+
+    def moved(self, copies):
+        old = self.np["pool"].copy(), None if self.scales is None else self.np["scales"].copy()
+        for s, d in copies:
+            self.np["pool"][d] = old[0][s]
+            if self.scales is not None:
+                self.np["scales"][d] = old[1][s]
+
+    def fork(self, parents, children, stream=None):
+        ca.cache_fork(self.t(parents), self.t(children), self.bt, self.lens, self.refs, self.pool, self.scales, status=self.status,
+                      stream=stream)
+        self.moved(oc.fork(parents, children, self.np["bt"], self.np["lens"], self.np["refs"]))
+
+    def free(self, rows):
+        ca.cache_free(self.t(rows), self.bt, self.lens, self.refs, status=self.status)
+        oc.free(rows, self.np["bt"], self.np["lens"], self.np["refs"])
+
+    def compact(self, workspace=None):
+        ca.cache_compact(self.bt, self.lens, self.refs, self.pool, self.scales, workspace=workspace, status=self.status)
+        self.moved(oc.compact(self.np["bt"], self.np["lens"], self.np["refs"]))
+
+    def check(self, status=0):
+        torch.cuda.synchronize()
+        assert int(self.status) == status
+        np.testing.assert_array_equal(self.lens.cpu().numpy(), self.np["lens"])
+        np.testing.assert_array_equal(self.refs.cpu().numpy(), self.np["refs"])
+        np.testing.assert_array_equal(self.bt.cpu().numpy(), self.np["bt"])
+        np.testing.assert_array_equal(self.pool.view(torch.uint8).cpu().numpy(), self.np["pool"])
+        if self.scales is not None:
+            np.testing.assert_array_equal(self.scales.cpu().numpy(), self.np["scales"])
+
+
+@pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("lens,times", [([1], 1), ([64], 2), ([65, 128, 63, 0], 2), ([1000, 77, 640, 5], 3)])
+def test_fork(dev, lens, times, q8):
+    n = len(lens) * times
+    w = World(lens, sum(oc.pages_of(x) for x in lens) + n, dev, q8, rows=len(lens) + n, seed=n)
+    w.fork([i % len(lens) for i in range(n)], list(range(len(lens) + n - 1, len(lens) - 1, -1)))
+    w.check()
+
+
+def test_fork_of_many_rows_and_of_forks(dev):
+    w = World([100] * 10, 1200, dev, rows=1034, seed=4)
+    w.fork([i % 10 for i in range(1024)], list(range(10, 1034)))
+    w.check()
+    w = World([200, 64], 40, dev, rows=8, seed=5)
+    w.fork([0, 0], [2, 3])
+    w.fork([2, 3, 1], [4, 5, 6])
+    w.free([0, 2])
+    w.fork([4], [0])
+    w.check()
+
+
+def test_fork_refusals(dev):
+    """Rows outside the batch, a child in use, a child named twice, itself: left out. The rest goes on."""
+    w = World([100, 200, 30], 40, dev, rows=8, seed=6)
+    w.fork([0, 9, -1, 1, 1, 2, 0, 0], [3, 4, 4, 2, 5, 5, 8, 0])
+    w.check(ca.MLA_STATUS_BAD_ROW)
+    assert w.lens.tolist() == [100, 200, 30, 100, 0, 200, 0, 0]
+    # a pool without room: the first forks that need a page get the last ones; those that need none go on
+    w = World([100, 128, 30], 2 + 2 + 1 + 1, dev, rows=8, seed=7)
+    w.fork([0, 2, 1, 0], [3, 4, 5, 6])
+    w.check(ca.MLA_STATUS_NO_FREE_PAGE)
+    assert w.lens.tolist() == [100, 128, 30, 100, 0, 128, 0, 0]
+    # bad entries of the parent: in the last page, and among the full ones
+    w = World([100, 200], 40, dev, rows=4, seed=8)
+    w.bt[0, 1] = 40
+    w.bt[1, 0] = -2
+    ca.cache_fork(w.t([0, 1]), w.t([2, 3]), w.bt, w.lens, w.refs, w.pool, w.scales, status=w.status)
+    torch.cuda.synchronize()
+    assert int(w.status) == bd.MLA_STATUS_BAD_BLOCK_TABLE and w.lens.tolist() == [100, 200, 0, 200]
+    assert int(w.bt[3, 0]) == -2
+    # a parent's length past its table
+    w = World([100], 40, dev, rows=2, seed=8)
+    w.lens[0] = 64 * w.bt.shape[1] + 1
+    ca.cache_fork(w.t([0]), w.t([1]), w.bt, w.lens, w.refs, w.pool, w.scales, status=w.status)
+    torch.cuda.synchronize()
+    assert int(w.status) == ca.MLA_STATUS_BAD_ROW and int(w.lens[1]) == 0
+
+
+def test_free(dev):
+    w = World([100, 200, 30, 0, 64], 20, dev, seed=9)
+    w.free([1, 1, 3, 4])
+    w.check()
+    w.free([-1, 5, 0])
+    w.check(ca.MLA_STATUS_BAD_ROW)
+    w = World([100, 200], 20, dev, seed=9)
+    w.refs[w.bt[0, 1].long()] = 0
+    w.bt[1, 2] = 999
+    ca.cache_free(w.t([0, 1]), w.bt, w.lens, w.refs, status=w.status)
+    torch.cuda.synchronize()
+    assert int(w.status) == ca.MLA_STATUS_BAD_REF_COUNT | bd.MLA_STATUS_BAD_BLOCK_TABLE
+    assert int(w.refs.sum()) == 1 and int(w.refs.min()) == 0  # the page whose entry was lost stays counted
+
+
+@pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("lens,gone,extra", [([64], [], 0), ([64], [0], 3), ([300, 64, 1000, 5], [0], 0), ([300, 64, 1000, 5], [2, 1], 7),
+                                             ([640] * 12, [0, 3, 5, 6, 11], 200)])
+def test_free_then_compact(dev, lens, gone, extra, q8):
+    w = World(lens, sum(oc.pages_of(x) for x in lens) + extra, dev, q8, seed=len(lens) + extra)
+    if gone:
+        w.free(gone)
+    ws = ca.cache_compact_workspace(w.pool.shape[0], dev)
+    w.compact(ws)
+    w.check()
+    live = int((w.np["refs"] > 0).sum())
+    assert int(ws.view(torch.int32)[0]) == live and not w.refs[live:].any()
+    w.compact(ws)  # packed already: nothing moves
+    w.check()
+
+
+def test_compact_shared_pages_and_large_books(dev):
+    w = World([500, 200, 70], 300, dev, rows=9, seed=12)
+    w.fork([0, 0, 1, 2], [3, 4, 5, 6])
+    w.free([0, 2])
+    w.compact()
+    w.check()
+    # more pages than one pass of the planning block, with holes everywhere
+    nb = 9001
+    pool = torch.zeros(nb, 64, 1, 576, dtype=torch.uint8, device=dev)
+    pool[:, 0, 0, :4] = torch.arange(nb, dtype=torch.int32, device=dev).view(torch.uint8).view(nb, 4)
+    refs = torch.from_numpy((np.random.RandomState(3).rand(nb) < 0.4).astype(np.int32))
+    held = torch.nonzero(refs)[:, 0].int()
+    bt = held[torch.randperm(len(held), generator=torch.Generator().manual_seed(1))][None].contiguous()
+    lens = torch.tensor([64 * len(held)], dtype=torch.int32)
+    n_bt, n_refs = bt.numpy().copy(), refs.numpy().copy()
+    g = [x.to(dev) for x in (bt, lens, refs)]
+    scales = torch.arange(nb, dtype=torch.float32, device=dev)[:, None].contiguous()
+    ca.cache_compact(*g, pool.view(torch.float8_e4m3fn), scales)
+    torch.cuda.synchronize()
+    oc.compact(n_bt, lens.numpy(), n_refs)
+    np.testing.assert_array_equal(g[0].cpu().numpy(), n_bt)
+    np.testing.assert_array_equal(g[2].cpu().numpy(), n_refs)
+    # each row entry still leads to the page it had, and so does its scale
+    at = g[0][0].long()
+    assert torch.equal(pool[at, 0, 0, :4].contiguous().view(torch.int32)[:, 0].cpu(), bt[0])
+    assert torch.equal(scales[at, 0].cpu(), bt[0].float())
+
+
+def test_compact_reports_bad_books(dev):
+    w = World([300, 64], 20, dev, seed=13)
+    w.bt[0, 0] = 20
+    w.refs[w.bt[1, 0].long()] = 0
+    ca.cache_compact(w.bt, w.lens, w.refs, w.pool, w.scales, status=w.status)
+    torch.cuda.synchronize()
+    got = int(w.status)
+    assert got & bd.MLA_STATUS_BAD_BLOCK_TABLE and got & ~(bd.MLA_STATUS_BAD_BLOCK_TABLE | ca.MLA_STATUS_BAD_REF_COUNT) == 0
+
+
+@pytest.mark.parametrize("q8", [True, False])
+def test_copy_pages(dev, q8):
+    w = World([64 * 10], 30, dev, q8, seed=14)
+    src, dst = [0, 5, 5, -1, 29], [10, 11, 12, 13, 14]
+    ca.cache_copy_pages(w.t(src), w.t(dst), w.pool, w.scales, status=w.status)
+    w.moved([(s, d) for s, d in zip(src, dst) if s >= 0])
+    w.check()
+    ca.cache_copy_pages(w.t([30, 1, 2]), w.t([20, 30, -1]), w.pool, w.scales, status=w.status)
+    w.check(bd.MLA_STATUS_BAD_BLOCK_TABLE)
+
+
+def test_pages_stream_and_graph(dev):
+    w = World([100, 300], 40, dev, rows=6, seed=15)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    w.fork([0, 1], [2, 3], stream=s)
+    s.synchronize()
+    w.check()
+    ws = torch.empty(4096, dtype=torch.uint8, device=dev)
+    a = [w.t([2]), w.t([4])]
+    graph = torch.cuda.CUDAGraph()
+    books = [x.clone() for x in (w.bt, w.lens, w.refs)]
+    with torch.cuda.graph(graph):
+        ca.cache_fork(*a, w.bt, w.lens, w.refs, w.pool, w.scales, status=w.status, workspace=ws)
+    for x, y in zip((w.bt, w.lens, w.refs), books):
+        assert torch.equal(x, y)
+    graph.replay()
+    w.moved(oc.fork([2], [4], w.np["bt"], w.np["lens"], w.np["refs"]))
+    w.check()
