@@ -58,7 +58,7 @@ constexpr int kQ8Terms = 3;                     // e4m3 terms of P
 // x = 2^kQ8Bias p: the largest weight is 2^kQ8Bias, and a weight may grow
 // 2^kQ8Grow above it before O^T is rescaled; 2^(bias + grow) <= 448.
 constexpr float kQ8Bias = 4.0f;
-constexpr float kQ8Grow = 4.0f;
+constexpr float kQ8Grow = 4.8f;
 constexpr float kQ8MinBias = -60.0f;
 constexpr float kQ8Unset = -1e30f;              // running max before the first visible token
 
@@ -70,8 +70,6 @@ struct Q8Params : FwdParams {
 template <int NG>
 struct Q8Cfg {
     static constexpr int kColGroups = NG / 16;              // softmax groups of 4 warps x 16 columns
-    static constexpr int kG1 = NG == 16 ? 2 : 1;            // GEMM1 issuers = S^T accumulators
-    static constexpr int kG2 = 1;                           // GEMM2 issuers
     static constexpr int kFirstQ = 4;                       // warps 4..7 split Q
     static constexpr int kFirstSoftmax = 8;
     static constexpr int kThreads = 32 * (kFirstSoftmax + 4 * kColGroups);
@@ -101,7 +99,7 @@ struct Q8Cfg {
     static constexpr int kInlinePlanMaxBG = (kSlots - kQ8Boxes) * kQ8BoxBytes / 4 - 48;
     // TMEM columns
     static constexpr int kSCol = 0;
-    static constexpr int kOCol = 2 * kG1 * kQN;
+    static constexpr int kOCol = 2 * kQN;
     static constexpr int kTmemUsed = kOCol + kQ8Boxes * kNP;
     static_assert(kTmemUsed <= 512, "TMEM budget");
     static constexpr int kTmemCols = 512;
@@ -123,13 +121,23 @@ enum Q8Bar {
 static_assert(kQbCount <= Q8Cfg<16>::kNumBars, "barrier slots");
 
 // ------------------------------------------------------------------ PTX
-__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t accumulate) {
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+// D[tmem] (+)= A . B, kind::f8f6f4.  The descriptors come as their two words: only
+// the low one (the address) changes from MMA to MMA.
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                        uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 a, {%1, %2};\n\t"
+        "mov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 // Instruction descriptor of kind::f8f6f4 with e4m3 A/B and fp32 D.
@@ -323,108 +331,129 @@ __device__ void q8_split_q(const Q8Params& p, const int32_t* meta, uint8_t* smem
 }
 
 // ------------------------------------------------------------------ MMA issuers
-// S^T[128 x 2 NG] = K[128 x 576] . [Q_hi | Q_lo]^T.  Issuer 0 of two takes boxes
-// 0 and 1 and the RoPE box, issuer 1 boxes 2 and 3, each into its own accumulator.
+// The issuing warps run converged and elect a lane for each MMA: the operands of
+// tcgen05.mma are uniform registers, and in code that one thread runs alone the
+// compiler has to move every operand there.  Measured on B200 (cycles from one MMA to
+// the next): issued by a lone thread with computed descriptors 90, elected 40 (M = 128,
+// N = 32), 44 (N = 48), 48 (N = 64) and 56 (N = 96); K-major and MN-major operands, swizzled or
+// not, cost the same.
+
+// S^T[128 x 2 NG] = K[128 x 576] . [Q_hi | Q_lo]^T.
 template <int NG>
-__device__ void q8_gemm1(const Q8Params& p, const int32_t* meta, uint8_t* smem, uint32_t tmem, const Ctl& ctl, int issuer) {
+__device__ void q8_gemm1(const Q8Params& p, const int32_t* meta, uint8_t* smem, uint32_t tmem, const Ctl& ctl) {
     using C = Q8Cfg<NG>;
     constexpr uint32_t kIdesc = idesc_e4m3_f32(kQ8Step, C::kQN, 0, 0);
     const uint32_t bar0 = smem_addr(smem + C::kBarOff);
     const uint64_t a0 = smem_desc(smem_addr(smem + C::kBoxOff), 16, 1024, kSwizzle128);
     const uint64_t r0 = smem_desc(smem_addr(smem + C::kRopeOff), 16, 512, kSwizzle64);
     const uint64_t b0 = smem_desc(smem_addr(smem + C::kQOff), C::kQN * 16, 128, kSwizzleNone);
-    constexpr int kPer = kQ8Boxes / C::kG1;
+    const uint32_t a_hi = (uint32_t)(a0 >> 32), r_hi = (uint32_t)(r0 >> 32), b_hi = (uint32_t)(b0 >> 32);
+    const uint32_t b_lo = (uint32_t)b0;
     WorkIter it;
     it.init(meta, p);
     Item item;
-    uint32_t s_it = 0, q_it = 0;
+    uint32_t s_it = 0, q_it = 0, slot = 0, phase = 0;
     bool ok = true;
     while (ok && it.next(p, item)) {
-        ok = wait_bounded(bar0 + 8 * kQbQFull, q_it & 1, ctl);
+        ok = wait_warp(bar0 + 8 * kQbQFull, q_it & 1, ctl);
         if (!ok) break;
         for (int j = item.p0; j < item.p1; j += 2) {
             const int sb = s_it & 1;
-            ok = wait_bounded(bar0 + 8 * (kQbSEmpty0 + sb), ((s_it >> 1) & 1) ^ 1, ctl);
+            ok = wait_warp(bar0 + 8 * (kQbSEmpty0 + sb), ((s_it >> 1) & 1) ^ 1, ctl);
             if (!ok) break;
-            tc_fence_after();
-            const uint32_t d = tmem + C::kSCol + (sb * C::kG1 + issuer) * C::kQN;
-            uint32_t acc = 0;
-#pragma unroll 1
-            for (int c = issuer * kPer; c < (issuer + 1) * kPer; ++c) {
-                const uint32_t n = s_it * kQ8Boxes + c, slot = n % C::kSlots;
-                ok = wait_bounded(bar0 + 8 * (kQbFull0 + slot), (n / C::kSlots) & 1, ctl);
+            const uint32_t d = tmem + C::kSCol + sb * C::kQN;
+#pragma unroll
+            for (int c = 0; c < kQ8Boxes; ++c) {
+                ok = wait_warp(bar0 + 8 * (kQbFull0 + slot), phase, ctl);
                 if (!ok) break;
                 tc_fence_after();
+                const uint32_t a_lo = (uint32_t)a0 + slot * (kQ8BoxBytes >> 4);
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    umma_f8(d, a0 + ((slot * kQ8BoxBytes + k * 32) >> 4), b0 + ((8 * c + 2 * k) * C::kQN), kIdesc, acc);
-                    acc = 1;
+                    for (int k = 0; k < 4; ++k)
+                        umma_f8(d, a_lo + 2 * k, a_hi, b_lo + (8 * c + 2 * k) * C::kQN, b_hi, kIdesc, c + k > 0);
+                }
+                __syncwarp();
+                if (++slot == C::kSlots) {
+                    slot = 0;
+                    phase ^= 1;
                 }
             }
             if (!ok) break;
-            if (issuer == 0) {
-                const uint32_t slot = s_it % kQ8RopeSlots;
-                ok = wait_bounded(bar0 + 8 * (kQbRopeFull0 + slot), (s_it / kQ8RopeSlots) & 1, ctl);
-                if (!ok) break;
-                tc_fence_after();
+            const uint32_t rs = s_it % kQ8RopeSlots;
+            ok = wait_warp(bar0 + 8 * (kQbRopeFull0 + rs), (s_it / kQ8RopeSlots) & 1, ctl);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t r_lo = (uint32_t)r0 + rs * (kQ8RopeBytes >> 4);
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
-                    umma_f8(d, r0 + ((slot * kQ8RopeBytes + k * 32) >> 4), b0 + ((8 * kQ8Boxes + 2 * k) * C::kQN), kIdesc, 1);
-                umma_commit(bar0 + 8 * (kQbRopeEmpty0 + slot));
+                    umma_f8(d, r_lo + 2 * k, r_hi, b_lo + (8 * kQ8Boxes + 2 * k) * C::kQN, b_hi, kIdesc, 1);
+                umma_commit(bar0 + 8 * (kQbRopeEmpty0 + rs));
+                umma_commit(bar0 + 8 * (kQbSFull0 + sb));
+                if (j + 2 >= item.p1) umma_commit(bar0 + 8 * kQbQEmpty);
             }
-            umma_commit(bar0 + 8 * (kQbSFull0 + sb));
-            if (j + 2 >= item.p1) umma_commit(bar0 + 8 * kQbQEmpty);
+            __syncwarp();
             ++s_it;
         }
         ++q_it;
     }
-    umma_commit(bar0 + 8 * kQbDone1);  // drained before TMEM is released
-    wait_drain(bar0 + 8 * kQbDone1, 0);
 }
 
 // O^T chunk c [128 x 3 NG] += V^T (box c, read MN-major) . P^T (MN-major without
 // swizzle: 16-byte pieces of 16 columns, 128 tokens apart by 2 KB).
 template <int NG>
-__device__ void q8_gemm2(const Q8Params& p, const int32_t* meta, uint8_t* smem, uint32_t tmem, const Ctl& ctl, int issuer) {
+__device__ void q8_gemm2(const Q8Params& p, const int32_t* meta, uint8_t* smem, uint32_t tmem, const Ctl& ctl) {
     using C = Q8Cfg<NG>;
     constexpr uint32_t kIdesc = idesc_e4m3_f32(128, C::kNP, 1, 1);
     const uint32_t bar0 = smem_addr(smem + C::kBarOff);
     const uint64_t a0 = smem_desc(smem_addr(smem + C::kBoxOff), kQ8BoxBytes, 1024, kSwizzle128);
     const uint64_t b0 = smem_desc(smem_addr(smem + C::kPOff), 128, kQ8Step * 16, kSwizzleNone);
-    constexpr int kPer = kQ8Boxes / C::kG2;
+    const uint32_t a_hi = (uint32_t)(a0 >> 32), b_hi = (uint32_t)(b0 >> 32);
     WorkIter it;
     it.init(meta, p);
     Item item;
-    uint32_t s_it = 0, item_it = 0;
+    uint32_t s_it = 0, item_it = 0, slot = 0;
     bool ok = true;
     while (ok && it.next(p, item)) {
         for (int j = item.p0; j < item.p1; j += 2) {
             const int pb = s_it & 1;
-            ok = wait_bounded(bar0 + 8 * (kQbPFull0 + pb), (s_it >> 1) & 1, ctl);
+            ok = wait_warp(bar0 + 8 * (kQbPFull0 + pb), (s_it >> 1) & 1, ctl);
             if (!ok) break;
             if (j == item.p0) {
-                ok = wait_bounded(bar0 + 8 * kQbOEmpty, (item_it & 1) ^ 1, ctl);
+                ok = wait_warp(bar0 + 8 * kQbOEmpty, (item_it & 1) ^ 1, ctl);
                 if (!ok) break;
             }
             tc_fence_after();
+            const uint32_t b_lo = (uint32_t)b0 + pb * (C::kPBytes >> 4);
+            const uint32_t more = j == item.p0 ? 0u : 1u;
 #pragma unroll
-            for (int cc = 0; cc < kPer; ++cc) {
-                const int c = issuer * kPer + cc;
-                const uint32_t slot = (s_it * kQ8Boxes + c) % C::kSlots;
+            for (int c = 0; c < kQ8Boxes; ++c) {
+                const uint32_t a_lo = (uint32_t)a0 + slot * (kQ8BoxBytes >> 4);
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < kQ8Step / 32; ++k)
-                    umma_f8(tmem + C::kOCol + c * C::kNP, a0 + ((slot * kQ8BoxBytes + k * 4096) >> 4),
-                            b0 + ((pb * C::kPBytes + k * 512) >> 4), kIdesc, (j == item.p0 && k == 0) ? 0u : 1u);
-                umma_commit(bar0 + 8 * (kQbEmpty0 + slot));
+                    for (int k = 0; k < kQ8Step / 32; ++k)
+                        umma_f8(tmem + C::kOCol + c * C::kNP, a_lo + k * (4096 >> 4), a_hi, b_lo + k * (512 >> 4), b_hi, kIdesc,
+                                k == 0 ? more : 1u);
+                    umma_commit(bar0 + 8 * (kQbEmpty0 + slot));
+                    if (c + 1 == kQ8Boxes) umma_commit(bar0 + 8 * (kQbPEmpty0 + pb));
+                }
+                __syncwarp();
+                if (++slot == C::kSlots) slot = 0;
             }
-            umma_commit(bar0 + 8 * (kQbPEmpty0 + pb));
             ++s_it;
         }
         if (!ok) break;
         ++item_it;
     }
-    umma_commit(bar0 + 8 * kQbDone2);
-    wait_drain(bar0 + 8 * kQbDone2, 0);
+}
+
+// What an issuing warp's MMAs still write is done before TMEM is released, on the
+// normal and the abort path alike (a commit with nothing outstanding arrives at once).
+__device__ __forceinline__ void q8_drain(uint32_t bar) {
+    if (elect_one()) umma_commit(bar);
+    __syncwarp();
+    wait_drain(bar, 0);
 }
 
 // ------------------------------------------------------------------ softmax
@@ -476,14 +505,16 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
         mbar_arrive(bar0 + 8 * kQbQSeen);
         const float4* qs4 = reinterpret_cast<const float4*>(qs_ring + (item_it & 1) * NG);
         const int gc0 = item.g * NG + cg * 16;  // first query column of the group
-        // scales of the item's pages, fetched a step ahead
-        auto page_scale = [&](int j) -> float {
-            if (j >= item.p1) j = item.p1 - 1;
-            const int phys = __ldg(p.block_table + (size_t)item.b * p.max_blocks + j);
+        // Table entries are fetched two steps ahead and page scales one, so
+        // that no step waits for either.
+        const int32_t* bt = p.block_table + (size_t)item.b * p.max_blocks;
+        auto entry = [&](int j) { return __ldg(bt + (j < item.p1 ? j : item.p1 - 1)); };
+        auto page_scale = [&](int phys) -> float {
             // (a page of scale 0 holds zeros; the floor keeps its tokens' weights finite)
             return fmaxf(__ldg(p.kv_scales + ((unsigned)phys < (unsigned)p.num_blocks ? phys : 0)), 1e-30f);
         };
-        float sc0 = page_scale(item.p0), sc1 = page_scale(item.p0 + 1);
+        float sc0 = page_scale(entry(item.p0)), sc1 = page_scale(entry(item.p0 + 1));
+        int ph0 = entry(item.p0 + 2), ph1 = entry(item.p0 + 3);
         float m[16], l[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
@@ -492,7 +523,9 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
         }
         float R = fmaxf(sc0, sc1);
         for (int j = item.p0; j < item.p1; j += 2) {
-            const float nx0 = page_scale(j + 2), nx1 = page_scale(j + 3);
+            const float nx0 = page_scale(ph0), nx1 = page_scale(ph1);
+            ph0 = entry(j + 4);
+            ph1 = entry(j + 5);
             const float ks = wq < 2 ? sc0 : sc1;  // this token's page
             const int sb = s_it & 1;
             ok = wait_warp(bar0 + 8 * (kQbSFull0 + sb), (s_it >> 1) & 1, ctl);
@@ -501,22 +534,10 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             float z[16];
             {
                 float lo[16];
-                const uint32_t s = tm + C::kSCol + sb * C::kG1 * C::kQN + cg * 16;
+                const uint32_t s = tm + C::kSCol + sb * C::kQN + cg * 16;
                 tmem_ld_x16(s, z);
                 tmem_ld_x16(s + NG, lo);
-                if constexpr (C::kG1 == 2) {
-                    float z2[16], lo2[16];
-                    tmem_ld_x16(s + C::kQN, z2);
-                    tmem_ld_x16(s + C::kQN + NG, lo2);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        z[c] += z2[c];
-                        lo[c] += lo2[c];
-                    }
-                } else {
-                    tmem_ld_wait();
-                }
+                tmem_ld_wait();
                 tc_fence_before();
                 mbar_arrive(bar0 + 8 * (kQbSEmpty0 + sb));
 #pragma unroll
@@ -589,14 +610,19 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int i = 0; i < kQ8Boxes * kQ8Terms; ++i) {
-                        float o[16];
+                    for (int i = 0; i < kQ8Boxes * kQ8Terms; i += 2) {
+                        float o[16], o1[16];
                         const uint32_t ta = tm + C::kOCol + i * NG + cg * 16;
                         tmem_ld_x16(ta, o);
+                        tmem_ld_x16(ta + NG, o1);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) o[c] *= alpha[c];
+                        for (int c = 0; c < 16; ++c) {
+                            o[c] *= alpha[c];
+                            o1[c] *= alpha[c];
+                        }
                         tmem_st_x16(ta, o);
+                        tmem_st_x16(ta + NG, o1);
                     }
                     tmem_st_wait();
                 }
@@ -731,8 +757,6 @@ __global__ void __launch_bounds__(Q8Cfg<NG>::kThreads, 1)
             if (i == kQbSEmpty0 || i == kQbSEmpty1 || i == kQbPFull0 || i == kQbPFull1 || i == kQbOEmpty || i == kQbQSeen)
                 count = kSm;
             if ((i >= kQbVote0 && i < kQbRopeFull0) || i == kQbQFull) count = 128;
-            if (i == kQbSFull0 || i == kQbSFull1 || i == kQbQEmpty || i == kQbDone1) count = C::kG1;
-            if (i == kQbPEmpty0 || i == kQbPEmpty1 || i == kQbDone2) count = C::kG2;
             mbar_init(bar0 + 8 * i, count);
         }
         *abort_flag = 0;
@@ -797,10 +821,12 @@ __global__ void __launch_bounds__(Q8Cfg<NG>::kThreads, 1)
     const Ctl ctl{abort_flag, p.status};
     if (warp == 0) {
         if (lane == 0) q8_producer<NG>(&kv_map, &rope_map, p, meta, smem, ctl, first_issued);
-    } else if (warp <= C::kG1) {
-        if (lane == 0) q8_gemm1<NG>(p, meta, smem, tmem, ctl, warp - 1);
-    } else if (warp == 3) {
-        if (lane == 0) q8_gemm2<NG>(p, meta, smem, tmem, ctl, 0);
+    } else if (warp == 1) {
+        q8_gemm1<NG>(p, meta, smem, tmem, ctl);
+        q8_drain(bar0 + 8 * kQbDone1);
+    } else if (warp == 2) {
+        q8_gemm2<NG>(p, meta, smem, tmem, ctl);
+        q8_drain(bar0 + 8 * kQbDone2);
     } else if (warp >= C::kFirstSoftmax) {
         q8_softmax<NG>(p, meta, smem, tmem, ctl);
     } else if (warp >= C::kFirstQ) {
