@@ -8,6 +8,7 @@ of libmla_decode.so, and there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -107,18 +108,55 @@ def mla_cache_version() -> int:
     return int(lib().mla_cache_version())
 
 
+# Small calls are bound by the host, so the checks below build no text and no tuples
+# unless they fail, and structures that only hold sizes are made once per size.
+_BF16, _F32, _E4M3, _I32 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _fail(msg: str, *args) -> None:
+    raise ValueError(msg % args if args else msg)
+
+
 def _i32(t: torch.Tensor, shape, what: str, device) -> None:
-    _require(t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == tuple(shape),
-             "%s must be contiguous int32 %s" % (what, list(shape)))
-    _require(t.device == device, "%s must be on %s" % (what, device))
+    if t.dtype is not _I32 or t.shape != shape or not t.is_contiguous():
+        _fail("%s must be contiguous int32 %s", what, list(shape))
+    if t.device != device:
+        _fail("%s must be on %s", what, device)
 
 
-def _on_current(device: torch.device, stream) -> None:
-    """The library launches on the current device; a stream carries its own."""
-    dev = stream.device if isinstance(stream, torch.cuda.Stream) else None
-    _require(device.type == "cuda", "tensors must be on a CUDA device")
-    _require(device.index == torch.cuda.current_device() and (dev is None or dev == device),
-             "tensors and stream must be of the current CUDA device")
+def _launch_stream(device: torch.device, stream) -> int:
+    """The stream's handle.  The library launches on the current device, so the
+    tensors and the stream must be of that device."""
+    if device.type != "cuda":
+        _fail("tensors must be on a CUDA device")
+    if device.index != torch.cuda.current_device():
+        _fail("tensors must be on the current CUDA device")
+    if stream is None:
+        return _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device != device:
+            _fail("stream must be of the current CUDA device")
+        return stream.cuda_stream
+    return int(stream)
+
+
+def _status(status: Optional[torch.Tensor], device) -> Optional[int]:
+    if status is None:
+        return None
+    if status.dtype is not _I32 or status.numel() < 1 or not status.is_contiguous() or status.device != device:
+        _fail("status must be int32 on %s", device)
+    return status.data_ptr()
+
+
+@functools.lru_cache(maxsize=1024)
+def _cache_dims(batch: int, max_blocks: int, num_blocks: int, dtype: int):
+    return ctypes.byref(mla_cache_dims(batch, max_blocks, num_blocks, bd.PAGE_SIZE, bd.D_QK, dtype))
+
+
+@functools.lru_cache(maxsize=1024)
+def _rope_dims(*sizes):
+    return ctypes.byref(mla_rope_dims(*sizes))
 
 
 # ---------------------------------------------------------------- rotary positions
@@ -145,60 +183,60 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, rope: mla_rope_table, o
     may be strided (multiples of 8 values); ``out=x`` rotates in place.
     ``transpose`` applies the transposed map: the gradient of x from that of
     the result."""
-    _require(x.dim() in (2, 3), "x must be [T, h, W] or [T, W]")
-    _require(x.dtype in (torch.bfloat16, torch.float32), "x must be bf16 or fp32")
+    shape, dtype, device = x.shape, x.dtype, x.device
+    if len(shape) not in (2, 3):
+        _fail("x must be [T, h, W] or [T, W]")
+    if dtype is not _BF16 and dtype is not _F32:
+        _fail("x must be bf16 or fp32")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _require(out.shape == x.shape and out.dtype == x.dtype and out.device == x.device,
-             "out must have the shape, type and device of x")
-    T, W = x.shape[0], x.shape[-1]
-    h = x.shape[1] if x.dim() == 3 else 1
-    _i32(positions, (T,), "positions", x.device)
+        out = torch.empty(shape, dtype=dtype, device=device)
+    elif out.shape != shape or out.dtype is not dtype or out.device != device:
+        _fail("out must have the shape, type and device of x")
+    T, W = shape[0], shape[-1]
+    h = shape[1] if len(shape) == 3 else 1
+    _i32(positions, (T,), "positions", device)
     if T == 0 or h == 0:
         return out
-    _require(x.stride(-1) == 1 and out.stride(-1) == 1, "the columns of x and out must be contiguous")
-    _on_current(x.device, stream)
-
-    def strides(t):  # (a dimension of one row has no stride of its own)
-        hs = t.stride(1) if t.dim() == 3 and h > 1 else W
-        return (t.stride(0) if T > 1 else h * hs), hs
-
-    d = mla_rope_dims(T, h, W, int(offset), *strides(x), *strides(out),
-                      MLA_DTYPE_BF16 if x.dtype == torch.bfloat16 else MLA_DTYPE_FP32, int(bool(transpose)))
-    _check(lib().mla_rope_apply(ctypes.byref(d), ctypes.byref(rope), _ptr(x), _ptr(positions), _ptr(out), _stream(stream)),
-           "mla_rope_apply")
+    xs, os_ = x.stride(), out.stride()
+    if xs[-1] != 1 or os_[-1] != 1:
+        _fail("the columns of x and out must be contiguous")
+    stream = _launch_stream(device, stream)
+    # (a dimension of one row has no stride of its own)
+    xh, oh = (xs[1], os_[1]) if h > 1 else (W, W)
+    d = _rope_dims(T, h, W, int(offset), xs[0] if T > 1 else h * xh, xh, os_[0] if T > 1 else h * oh, oh,
+                   MLA_DTYPE_BF16 if dtype is _BF16 else MLA_DTYPE_FP32, int(bool(transpose)))
+    rc = lib().mla_rope_apply(d, ctypes.byref(rope), x.data_ptr(), positions.data_ptr(), out.data_ptr(), stream)
+    if rc:
+        _check(rc, "mla_rope_apply")
     return out
 
 
 # ---------------------------------------------------------------- the cache
-def _pool_dims(kv_cache: torch.Tensor, kv_scales: Optional[torch.Tensor], batch: int, max_blocks: int) -> mla_cache_dims:
-    nb = kv_cache.shape[0]
-    q8 = kv_cache.dtype == torch.float8_e4m3fn
-    _require((q8 or kv_cache.dtype == torch.bfloat16) and kv_cache.is_contiguous() and
-             tuple(kv_cache.shape) == (nb, bd.PAGE_SIZE, 1, bd.D_QK),
-             "kv_cache must be contiguous bf16 or float8_e4m3fn [num_blocks, 64, 1, 576]")
-    if q8:
-        _require(kv_scales is not None and kv_scales.dtype == torch.float32 and kv_scales.is_contiguous() and
-                 tuple(kv_scales.shape) == (nb, 1) and kv_scales.device == kv_cache.device,
-                 "kv_scales must be contiguous fp32 [num_blocks, 1] beside an 8-bit cache")
-    else:
-        _require(kv_scales is None, "a bf16 cache has no scales")
-    return mla_cache_dims(int(batch), int(max_blocks), int(nb), bd.PAGE_SIZE, bd.D_QK,
-                          MLA_CACHE_E4M3 if q8 else MLA_CACHE_BF16)
+def _pool_dims(kv_cache: torch.Tensor, kv_scales: Optional[torch.Tensor], batch: int, max_blocks: int):
+    """The dims of a pool and its table, and the scales' address."""
+    shape, q8 = kv_cache.shape, kv_cache.dtype is _E4M3
+    nb = shape[0]
+    if not (q8 or kv_cache.dtype is _BF16) or shape != (nb, bd.PAGE_SIZE, 1, bd.D_QK) or not kv_cache.is_contiguous():
+        _fail("kv_cache must be contiguous bf16 or float8_e4m3fn [num_blocks, 64, 1, 576]")
+    if not q8:
+        if kv_scales is not None:
+            _fail("a bf16 cache has no scales")
+        return _cache_dims(batch, max_blocks, nb, MLA_CACHE_BF16), None
+    if kv_scales is None or kv_scales.dtype is not _F32 or kv_scales.shape != (nb, 1) or not kv_scales.is_contiguous() or \
+            kv_scales.device != kv_cache.device:
+        _fail("kv_scales must be contiguous fp32 [num_blocks, 1] beside an 8-bit cache")
+    return _cache_dims(batch, max_blocks, nb, MLA_CACHE_E4M3), kv_scales.data_ptr()
 
 
-def _books(block_table, cache_seqlens, ref_counts, nb, device) -> None:
-    _require(block_table.dim() == 2, "block_table must be int32 [B, max_blocks_per_seq]")
-    _i32(block_table, block_table.shape, "block_table", device)
-    _i32(cache_seqlens, (block_table.shape[0],), "cache_seqlens", device)
+def _books(block_table, cache_seqlens, ref_counts, nb, device) -> Tuple[int, int]:
+    shape = block_table.shape
+    if len(shape) != 2:
+        _fail("block_table must be int32 [B, max_blocks_per_seq]")
+    _i32(block_table, shape, "block_table", device)
+    _i32(cache_seqlens, shape[:1], "cache_seqlens", device)
     if ref_counts is not None:
         _i32(ref_counts, (nb,), "ref_counts", device)
-
-
-def _status(status: Optional[torch.Tensor], device) -> None:
-    if status is not None:
-        _require(status.dtype == torch.int32 and status.numel() >= 1 and status.is_contiguous() and status.device == device,
-                 "status must be int32 on %s" % device)
+    return shape[0], shape[1]
 
 
 def cache_append(c_kv: torch.Tensor, k_pe: torch.Tensor, new_offsets: torch.Tensor, block_table: torch.Tensor,
@@ -212,20 +250,24 @@ def cache_append(c_kv: torch.Tensor, k_pe: torch.Tensor, new_offsets: torch.Tens
     their positions.  An 8-bit cache's page scales follow its rows."""
     device = kv_cache.device
     T = c_kv.shape[0]
-    _books(block_table, cache_seqlens, None, 0, device)
-    d = _pool_dims(kv_cache, kv_scales, block_table.shape[0], block_table.shape[1])
-    for t, w, what in ((c_kv, bd.D_V, "c_kv"), (k_pe, bd.D_QK - bd.D_V, "k_pe")):
-        _require(t.dtype == torch.bfloat16 and t.dim() == 2 and tuple(t.shape) == (T, w) and
-                 (t.stride(1) == 1 or t.numel() == 0) and t.device == device, "%s must be bf16 [T, %d] on %s" % (what, w, device))
-    _i32(new_offsets, (block_table.shape[0] + 1,), "new_offsets", device)
-    _status(status, device)
+    B, width = _books(block_table, cache_seqlens, None, 0, device)
+    d, scales = _pool_dims(kv_cache, kv_scales, B, width)
+    cs, ps = c_kv.stride(), k_pe.stride()
+    if c_kv.dtype is not _BF16 or c_kv.shape != (T, bd.D_V) or (cs[1] != 1 and T) or c_kv.device != device:
+        _fail("c_kv must be bf16 [T, 512] on %s", device)
+    if k_pe.dtype is not _BF16 or k_pe.shape != (T, bd.D_QK - bd.D_V) or (ps[1] != 1 and T) or k_pe.device != device:
+        _fail("k_pe must be bf16 [T, 64] on %s, as many rows as c_kv", device)
+    _i32(new_offsets, (B + 1,), "new_offsets", device)
+    status = _status(status, device)
     if T == 0:
         return
-    _on_current(device, stream)
-    _check(lib().mla_cache_append(ctypes.byref(d), T, _ptr(c_kv), c_kv.stride(0) if T > 1 else bd.D_V, _ptr(k_pe),
-                                  k_pe.stride(0) if T > 1 else bd.D_QK - bd.D_V, _ptr(new_offsets),
-                                  None if rope is None else ctypes.byref(rope), _ptr(block_table), _ptr(cache_seqlens),
-                                  _ptr(kv_cache), _ptr(kv_scales), _ptr(status), _stream(stream)), "mla_cache_append")
+    stream = _launch_stream(device, stream)
+    rc = lib().mla_cache_append(d, T, c_kv.data_ptr(), cs[0] if T > 1 else bd.D_V, k_pe.data_ptr(),
+                                ps[0] if T > 1 else bd.D_QK - bd.D_V, new_offsets.data_ptr(),
+                                None if rope is None else ctypes.byref(rope), block_table.data_ptr(),
+                                cache_seqlens.data_ptr(), kv_cache.data_ptr(), scales, status, stream)
+    if rc:
+        _check(rc, "mla_cache_append")
 
 
 def cache_fork(parents: torch.Tensor, children: torch.Tensor, block_table: torch.Tensor, cache_seqlens: torch.Tensor,
@@ -235,18 +277,20 @@ def cache_fork(parents: torch.Tensor, children: torch.Tensor, block_table: torch
     pages are shared and counted, a last page that is not full is copied
     into the lowest free page."""
     device, n = kv_cache.device, parents.numel()
-    _books(block_table, cache_seqlens, ref_counts, kv_cache.shape[0], device)
-    d = _pool_dims(kv_cache, kv_scales, block_table.shape[0], block_table.shape[1])
+    B, width = _books(block_table, cache_seqlens, ref_counts, kv_cache.shape[0], device)
+    d, scales = _pool_dims(kv_cache, kv_scales, B, width)
     _i32(parents, (n,), "parents", device)
     _i32(children, (n,), "children", device)
-    _status(status, device)
+    status = _status(status, device)
     if n == 0:
         return
-    _on_current(device, stream)
-    workspace = _workspace(workspace, int(lib().mla_cache_fork_workspace_bytes(n)), device, stream)
-    _check(lib().mla_cache_fork(ctypes.byref(d), n, _ptr(parents), _ptr(children), _ptr(block_table), _ptr(cache_seqlens),
-                                _ptr(ref_counts), _ptr(kv_cache), _ptr(kv_scales), _ptr(workspace), _ptr(status),
-                                _stream(stream)), "mla_cache_fork")
+    raw = _launch_stream(device, stream)
+    workspace = _workspace(workspace, 12 * n, device, stream)
+    rc = lib().mla_cache_fork(d, n, parents.data_ptr(), children.data_ptr(), block_table.data_ptr(),
+                              cache_seqlens.data_ptr(), ref_counts.data_ptr(), kv_cache.data_ptr(), scales,
+                              workspace.data_ptr(), status, raw)
+    if rc:
+        _check(rc, "mla_cache_fork")
 
 
 def cache_free(rows: torch.Tensor, block_table: torch.Tensor, cache_seqlens: torch.Tensor, ref_counts: torch.Tensor,
@@ -254,49 +298,51 @@ def cache_free(rows: torch.Tensor, block_table: torch.Tensor, cache_seqlens: tor
     """Gives up the pages of ``rows`` and empties them (mla_cache_free)."""
     device, n = block_table.device, rows.numel()
     nb = ref_counts.numel()
-    _books(block_table, cache_seqlens, ref_counts, nb, device)
+    B, width = _books(block_table, cache_seqlens, ref_counts, nb, device)
     _i32(rows, (n,), "rows", device)
-    _status(status, device)
+    status = _status(status, device)
     if n == 0:
         return
-    _on_current(device, stream)
-    d = mla_cache_dims(block_table.shape[0], block_table.shape[1], nb, bd.PAGE_SIZE, bd.D_QK, MLA_CACHE_BF16)
-    _check(lib().mla_cache_free(ctypes.byref(d), n, _ptr(rows), _ptr(block_table), _ptr(cache_seqlens), _ptr(ref_counts),
-                                _ptr(status), _stream(stream)), "mla_cache_free")
+    stream = _launch_stream(device, stream)
+    rc = lib().mla_cache_free(_cache_dims(B, width, nb, MLA_CACHE_BF16), n, rows.data_ptr(), block_table.data_ptr(),
+                              cache_seqlens.data_ptr(), ref_counts.data_ptr(), status, stream)
+    if rc:
+        _check(rc, "mla_cache_free")
 
 
 def cache_copy_pages(src: torch.Tensor, dst: torch.Tensor, kv_cache: torch.Tensor, kv_scales: Optional[torch.Tensor] = None,
                      status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Page dst[i] of the pool = page src[i], with its scale (mla_cache_copy_pages)."""
     device, n = kv_cache.device, src.numel()
-    d = _pool_dims(kv_cache, kv_scales, 1, 1)
+    d, scales = _pool_dims(kv_cache, kv_scales, 1, 1)
     _i32(src, (n,), "src", device)
     _i32(dst, (n,), "dst", device)
-    _status(status, device)
+    status = _status(status, device)
     if n == 0:
         return
-    _on_current(device, stream)
-    _check(lib().mla_cache_copy_pages(ctypes.byref(d), n, _ptr(src), _ptr(dst), _ptr(kv_cache), _ptr(kv_scales),
-                                      _ptr(status), _stream(stream)), "mla_cache_copy_pages")
+    stream = _launch_stream(device, stream)
+    rc = lib().mla_cache_copy_pages(d, n, src.data_ptr(), dst.data_ptr(), kv_cache.data_ptr(), scales, status, stream)
+    if rc:
+        _check(rc, "mla_cache_copy_pages")
 
 
 def _workspace(workspace, need: int, device, stream) -> torch.Tensor:
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if isinstance(stream, torch.cuda.Stream):
-            workspace.record_stream(stream)  # it is dropped before the stream has run
-        else:
-            _require(stream is None, "a raw stream handle needs a workspace of the caller's")
-    _require(workspace.dtype == torch.uint8 and workspace.is_contiguous() and workspace.numel() >= need and
-             workspace.device == device, "workspace must be %d bytes (uint8) on %s" % (need, device))
+        if stream is not None:  # it is dropped before the stream has run
+            if not isinstance(stream, torch.cuda.Stream):
+                _fail("a raw stream handle needs a workspace of the caller's")
+            workspace.record_stream(stream)
+    elif workspace.dtype is not torch.uint8 or workspace.numel() < need or not workspace.is_contiguous() or \
+            workspace.device != device:
+        _fail("workspace must be %d bytes (uint8) on %s", need, device)
     return workspace
 
 
 def cache_compact_workspace(num_blocks: int, device) -> torch.Tensor:
     """A workspace for cache_compact on a pool of num_blocks pages; its first
     int32 is the number of pages in use after a call."""
-    d = mla_cache_dims(1, 1, int(num_blocks), bd.PAGE_SIZE, bd.D_QK, MLA_CACHE_BF16)
-    n = int(lib().mla_cache_compact_workspace_bytes(ctypes.byref(d)))
+    n = int(lib().mla_cache_compact_workspace_bytes(_cache_dims(1, 1, int(num_blocks), MLA_CACHE_BF16)))
     if n == 0:
         raise MlaDecodeError(bd.MLA_ERR_INVALID_ARG, "cache_compact_workspace")
     return torch.empty(n, dtype=torch.uint8, device=device)
@@ -307,13 +353,15 @@ def cache_compact(block_table: torch.Tensor, cache_seqlens: torch.Tensor, ref_co
                   status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Moves the pages in use to the front of the pool (mla_cache_compact)."""
     device, nb = kv_cache.device, kv_cache.shape[0]
-    _books(block_table, cache_seqlens, ref_counts, nb, device)
-    d = _pool_dims(kv_cache, kv_scales, block_table.shape[0], block_table.shape[1])
-    _status(status, device)
-    _on_current(device, stream)
-    workspace = _workspace(workspace, int(lib().mla_cache_compact_workspace_bytes(ctypes.byref(d))), device, stream)
-    _check(lib().mla_cache_compact(ctypes.byref(d), _ptr(block_table), _ptr(cache_seqlens), _ptr(ref_counts), _ptr(kv_cache),
-                                   _ptr(kv_scales), _ptr(workspace), _ptr(status), _stream(stream)), "mla_cache_compact")
+    B, width = _books(block_table, cache_seqlens, ref_counts, nb, device)
+    d, scales = _pool_dims(kv_cache, kv_scales, B, width)
+    status = _status(status, device)
+    raw = _launch_stream(device, stream)
+    workspace = _workspace(workspace, 16 + 8 * nb, device, stream)
+    rc = lib().mla_cache_compact(d, block_table.data_ptr(), cache_seqlens.data_ptr(), ref_counts.data_ptr(),
+                                 kv_cache.data_ptr(), scales, workspace.data_ptr(), status, raw)
+    if rc:
+        _check(rc, "mla_cache_compact")
 
 
 # ---------------------------------------------------------------- decode over the 8-bit cache
@@ -369,23 +417,25 @@ class Q8Decoder:
         self.out = torch.empty(batch, s_q, num_heads, bd.D_V, dtype=torch.float32 if fp32_out else torch.bfloat16,
                                device=self.device)
         self.lse = torch.empty(batch, num_heads, s_q, dtype=torch.float32, device=self.device)
+        self._schedule, self._workspace = self.schedule.data_ptr(), self.workspace.data_ptr()
+        self._out, self._lse = self.out.data_ptr(), self.lse.data_ptr()
+        self._q_shape = torch.Size((batch, s_q, num_heads, bd.D_QK))
+        self._kv_shape = torch.Size((num_blocks, bd.PAGE_SIZE, 1, bd.D_QK))
+        self._scales_shape = torch.Size((num_blocks, 1))
+        self._bt_shape = torch.Size((batch, max_blocks_per_seq))
 
     def check_inputs(self, q, kv_cache, kv_scales, block_table, cache_seqlens) -> None:
-        d = self.dims
-        _require(q.dtype == torch.bfloat16 and q.is_contiguous() and
-                 tuple(q.shape) == (d.batch, d.s_q, d.num_heads, bd.D_QK), "q must be bf16 [B, s_q, h, 576]")
-        _require(kv_cache.dtype == torch.float8_e4m3fn and kv_cache.is_contiguous() and
-                 tuple(kv_cache.shape) == (d.num_blocks, bd.PAGE_SIZE, 1, bd.D_QK),
-                 "kv_cache must be float8_e4m3fn [num_blocks, 64, 1, 576]")
-        _require(kv_scales.dtype == torch.float32 and kv_scales.is_contiguous() and
-                 tuple(kv_scales.shape) == (d.num_blocks, 1), "kv_scales must be fp32 [num_blocks, 1]")
-        _require(block_table.dtype == torch.int32 and block_table.is_contiguous() and
-                 tuple(block_table.shape) == (d.batch, d.max_blocks_per_seq),
-                 "block_table must be int32 [B, max_blocks_per_seq]")
-        _require(cache_seqlens.dtype == torch.int32 and cache_seqlens.is_contiguous() and
-                 tuple(cache_seqlens.shape) == (d.batch,), "cache_seqlens must be int32 [B]")
-        for t in (q, kv_cache, kv_scales, block_table, cache_seqlens):
-            _require(t.device == self.out.device, "all tensors must be on %s" % self.out.device)
+        device = self.out.device
+        if q.dtype is not _BF16 or q.shape != self._q_shape or not q.is_contiguous() or q.device != device:
+            _fail("q must be contiguous bf16 %s on %s", list(self._q_shape), device)
+        if kv_cache.dtype is not _E4M3 or kv_cache.shape != self._kv_shape or not kv_cache.is_contiguous() or \
+                kv_cache.device != device:
+            _fail("kv_cache must be contiguous float8_e4m3fn %s on %s", list(self._kv_shape), device)
+        if kv_scales.dtype is not _F32 or kv_scales.shape != self._scales_shape or not kv_scales.is_contiguous() or \
+                kv_scales.device != device:
+            _fail("kv_scales must be contiguous fp32 %s on %s", list(self._scales_shape), device)
+        _i32(block_table, self._bt_shape, "block_table", device)
+        _i32(cache_seqlens, self._bt_shape[:1], "cache_seqlens", device)
 
     def plan(self, cache_seqlens: torch.Tensor, stream=None) -> None:
         mla_decode_q8_get_schedule(self.dims, cache_seqlens, self.schedule, stream)
@@ -394,8 +444,12 @@ class Q8Decoder:
                  check: bool = True) -> Tuple[torch.Tensor, torch.Tensor]:
         if check:
             self.check_inputs(q, kv_cache, kv_scales, block_table, cache_seqlens)
-        mla_decode_q8_fwd(self.dims, self.schedule, self.workspace, q, kv_cache, kv_scales, block_table, cache_seqlens,
-                          softmax_scale, self.out, self.lse, stream)
+        rc = lib().mla_decode_q8_fwd(ctypes.byref(self.dims), self._schedule, self._workspace, q.data_ptr(),
+                                     kv_cache.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(),
+                                     cache_seqlens.data_ptr(), softmax_scale, self._out, self._lse,
+                                     _launch_stream(self.out.device, stream))
+        if rc:
+            _check(rc, "mla_decode_q8_fwd")
         return self.out, self.lse
 
     def status(self) -> int:

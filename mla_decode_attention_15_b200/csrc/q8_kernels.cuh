@@ -51,14 +51,17 @@ constexpr int kQ8Row = kDqk;                    // bytes per token
 constexpr int kQ8PageBytes = kPage * kQ8Row;    // 36,864
 constexpr int kQ8Step = 2 * kPage;              // tokens per step
 constexpr int kQ8BoxBytes = kQ8Step * 128;      // 128 tokens x 128 latent columns
+constexpr int kQ8SlotBytes = 2 * kQ8BoxBytes;   // ring slot: two boxes, half of a step's latent columns
 constexpr int kQ8RopeBytes = kQ8Step * 64;      // 128 tokens x 64 RoPE columns
 constexpr int kQ8Boxes = 4;
-constexpr int kQ8RopeSlots = 2;
+constexpr int kQ8Halves = 2;                    // slots per step
 constexpr int kQ8Terms = 3;                     // e4m3 terms of P
 // x = 2^kQ8Bias p: the largest weight is 2^kQ8Bias, and a weight may grow
 // 2^kQ8Grow above it before O^T is rescaled; 2^(bias + grow) <= 448.
 constexpr float kQ8Bias = 4.0f;
 constexpr float kQ8Grow = 4.8f;
+// The Q warps wait for most of an item; they leave the issue slots alone meanwhile.
+constexpr int kQ8Nap = 200, kQ8MaxNaps = 1 << 22;  // ns; about a second
 constexpr float kQ8MinBias = -60.0f;
 constexpr float kQ8Unset = -1e30f;              // running max before the first visible token
 
@@ -73,13 +76,19 @@ struct Q8Cfg {
     static constexpr int kFirstQ = 4;                       // warps 4..7 split Q
     static constexpr int kFirstSoftmax = 8;
     static constexpr int kThreads = 32 * (kFirstSoftmax + 4 * kColGroups);
+    // 512 threads leave 128 registers each at launch: the issuing and the Q warps give
+    // some of theirs to the softmax (warpgroups: issue, Q, softmax twice).
+    static constexpr bool kSplitRegs = kThreads == 512;
+    static constexpr int kRegsIssue = 64, kRegsQ = 96, kRegsSoftmax = 176;
+    static_assert(!kSplitRegs || kRegsIssue + kRegsQ + 2 * kRegsSoftmax <= 4 * 128, "register split");
     static constexpr int kQN = 2 * NG;                      // S^T columns: hi, lo
     static constexpr int kNP = kQ8Terms * NG;               // O^T columns per d_v chunk
-    static constexpr int kSlots = NG == 16 ? 11 : 9;        // ring of 16 KB boxes
+    static constexpr int kSlots = NG == 16 ? 5 : 4;         // ring of 32 KB slots
+    static constexpr int kRopeSlots = NG == 16 ? 3 : 2;     // one per step that the ring can hold, in part or whole
     // shared memory
     static constexpr int kBoxOff = 0;
-    static constexpr int kRopeOff = kBoxOff + kSlots * kQ8BoxBytes;
-    static constexpr int kQOff = kRopeOff + kQ8RopeSlots * kQ8RopeBytes;
+    static constexpr int kRopeOff = kBoxOff + kSlots * kQ8SlotBytes;
+    static constexpr int kQOff = kRopeOff + kRopeSlots * kQ8RopeBytes;
     static constexpr int kQBytes = kQN * kDqk;
     static constexpr int kPOff = kQOff + kQBytes;
     static constexpr int kPBytes = kQ8Step * kNP;
@@ -96,7 +105,7 @@ struct Q8Cfg {
     static_assert(kAlloc <= 227 * 1024, "shared memory budget");
     static_assert(kQOff % 1024 == 0 && kPOff % 128 == 0 && kPBytes % 128 == 0, "operand alignment");
     // the plan's scratch: slots past the first step's boxes
-    static constexpr int kInlinePlanMaxBG = (kSlots - kQ8Boxes) * kQ8BoxBytes / 4 - 48;
+    static constexpr int kInlinePlanMaxBG = (kSlots - kQ8Halves) * kQ8SlotBytes / 4 - 48;
     // TMEM columns
     static constexpr int kSCol = 0;
     static constexpr int kOCol = 2 * kQN;
@@ -105,16 +114,14 @@ struct Q8Cfg {
     static constexpr int kTmemCols = 512;
 };
 
-constexpr int kQ8MaxSlots = 11;
+constexpr int kQ8MaxSlots = 5;
 enum Q8Bar {
     kQbQFull = 0, kQbQEmpty, kQbSFull0, kQbSFull1, kQbSEmpty0, kQbSEmpty1, kQbPFull0, kQbPFull1, kQbPEmpty0, kQbPEmpty1,
     kQbOEmpty, kQbDone1, kQbDone2, kQbQSeen,
     kQbVote0,                            // [2 parities][2 column groups]
     kQbMax0 = kQbVote0 + 4,              // [2 column groups]
     kQbSum0 = kQbMax0 + 2,               // [2 column groups]
-    kQbRopeFull0 = kQbSum0 + 2,
-    kQbRopeEmpty0 = kQbRopeFull0 + kQ8RopeSlots,
-    kQbFull0 = kQbRopeEmpty0 + kQ8RopeSlots,
+    kQbFull0 = kQbSum0 + 2,
     kQbEmpty0 = kQbFull0 + kQ8MaxSlots,
     kQbCount = kQbEmpty0 + kQ8MaxSlots
 };
@@ -181,15 +188,27 @@ __device__ __forceinline__ int q8_page(const Q8Params& p, const Item& item, int 
     return phys;
 }
 
-// Loads box c (< 4: latent columns, 4: RoPE) of a step of one or two pages.
-__device__ __forceinline__ void q8_load(const CUtensorMap* kv_map, const CUtensorMap* rope_map, uint32_t dst, uint32_t bar,
-                                        int c, int ph0, int ph1, uint64_t policy) {
-    const bool rope = c == kQ8Boxes;
-    const uint32_t half = rope ? kQ8RopeBytes / 2 : kQ8BoxBytes / 2;
-    mbar_arrive_expect_tx(bar, ph1 >= 0 ? 2 * half : half);
-    const CUtensorMap* map = rope ? rope_map : kv_map;
-    tma_load_3d_hint(dst, map, bar, 128 * c, 0, ph0, policy);
-    if (ph1 >= 0) tma_load_3d_hint(dst + half, map, bar, 128 * c, 0, ph1, policy);
+// Loads half hf of a step of one or two pages into a ring slot: boxes 2 hf and
+// 2 hf + 1, and with the second half the RoPE columns.
+template <int NG>
+__device__ __forceinline__ void q8_load(const CUtensorMap* kv_map, const CUtensorMap* rope_map, uint8_t* smem, uint32_t slot,
+                                        uint32_t rope_slot, int hf, int ph0, int ph1, uint64_t policy) {
+    using C = Q8Cfg<NG>;
+    const uint32_t bar = smem_addr(smem + C::kBarOff) + 8 * (kQbFull0 + slot);
+    const uint32_t dst = smem_addr(smem + C::kBoxOff) + slot * kQ8SlotBytes;
+    const uint32_t page = kQ8SlotBytes / 2 + (hf ? kQ8RopeBytes / 2 : 0);  // bytes of one page
+    mbar_arrive_expect_tx(bar, ph1 >= 0 ? 2 * page : page);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        tma_load_3d_hint(dst + c * kQ8BoxBytes, kv_map, bar, 128 * (2 * hf + c), 0, ph0, policy);
+        if (ph1 >= 0)
+            tma_load_3d_hint(dst + c * kQ8BoxBytes + kQ8BoxBytes / 2, kv_map, bar, 128 * (2 * hf + c), 0, ph1, policy);
+    }
+    if (hf) {
+        const uint32_t rd = smem_addr(smem + C::kRopeOff) + rope_slot * kQ8RopeBytes;
+        tma_load_3d_hint(rd, rope_map, bar, kDv, 0, ph0, policy);
+        if (ph1 >= 0) tma_load_3d_hint(rd + kQ8RopeBytes / 2, rope_map, bar, kDv, 0, ph1, policy);
+    }
 }
 
 template <int NG>
@@ -197,47 +216,38 @@ __device__ void q8_producer(const CUtensorMap* kv_map, const CUtensorMap* rope_m
                             uint8_t* smem, const Ctl& ctl, bool first_issued) {
     using C = Q8Cfg<NG>;
     const uint32_t bar0 = smem_addr(smem + C::kBarOff);
-    const uint32_t box0 = smem_addr(smem + C::kBoxOff), rope0 = smem_addr(smem + C::kRopeOff);
     const uint64_t policy = p.share > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
     WorkIter it;
     it.init(meta, p);
     Item item;
-    uint32_t n = 0, r = 0;                 // boxes and RoPE boxes issued (or left out by the test hook)
+    uint32_t n = 0, rope = 0;              // halves issued (or left out by the test hook)
     const bool stall = p.test_stall != 0;
     bool ok = true;
     while (ok && it.next(p, item)) {
         for (int j = item.p0; ok && j < item.p1; j += 2) {
-            if (r == 0 && (first_issued || stall)) {  // issued before the wait on the previous grid, or left out
-                n = kQ8Boxes;
-                r = 1;
+            if (n == 0 && (first_issued || stall)) {  // issued before the wait on the previous grid, or left out
+                n = kQ8Halves;
+                rope = 1;
                 continue;
             }
             const int ph0 = q8_page(p, item, j);
             const int ph1 = j + 1 < item.p1 ? q8_page(p, item, j + 1) : -1;
 #pragma unroll 1
-            for (int c = 0; c < kQ8Boxes; ++c, ++n) {
+            for (int hf = 0; hf < kQ8Halves; ++hf, ++n) {
                 const uint32_t slot = n % C::kSlots;
+                // (a step's RoPE slot is free when the slots of the step kRopeSlots before are)
                 ok = wait_bounded(bar0 + 8 * (kQbEmpty0 + slot), ((n / C::kSlots) & 1) ^ 1, ctl);
                 if (!ok) break;
-                q8_load(kv_map, rope_map, box0 + slot * kQ8BoxBytes, bar0 + 8 * (kQbFull0 + slot), c, ph0, ph1, policy);
+                q8_load<NG>(kv_map, rope_map, smem, slot, rope, hf, ph0, ph1, policy);
             }
-            if (!ok) break;
-            const uint32_t slot = r % kQ8RopeSlots;
-            ok = wait_bounded(bar0 + 8 * (kQbRopeEmpty0 + slot), ((r / kQ8RopeSlots) & 1) ^ 1, ctl);
-            if (!ok) break;
-            q8_load(kv_map, rope_map, rope0 + slot * kQ8RopeBytes, bar0 + 8 * (kQbRopeFull0 + slot), kQ8Boxes, ph0, ph1, policy);
-            ++r;
+            if (++rope == C::kRopeSlots) rope = 0;
         }
     }
     if (!ok) {
         // Let the copies already issued land before the CTA exits.
         for (uint32_t k = 0; k < C::kSlots; ++k) {
             const uint32_t count = n > k ? (n - k + C::kSlots - 1) / C::kSlots : 0;
-            if (count > (stall && k < kQ8Boxes ? 1u : 0u)) wait_drain(bar0 + 8 * (kQbFull0 + k), (count - 1) & 1);
-        }
-        for (uint32_t k = 0; k < kQ8RopeSlots; ++k) {
-            const uint32_t count = r > k ? (r - k + kQ8RopeSlots - 1) / kQ8RopeSlots : 0;
-            if (count > (stall && k == 0 ? 1u : 0u)) wait_drain(bar0 + 8 * (kQbRopeFull0 + k), (count - 1) & 1);
+            if (count > (stall && k < kQ8Halves ? 1u : 0u)) wait_drain(bar0 + 8 * (kQbFull0 + k), (count - 1) & 1);
         }
     }
 }
@@ -293,6 +303,8 @@ __device__ void q8_split_q(const Q8Params& p, const int32_t* meta, uint8_t* smem
                 // GEMM1 of the previous item has read its Q, and its softmax has
                 // begun (so it is past its wait on kQbQFull, and done with the
                 // row scales of the item before).
+                for (int i = 0; i < kQ8MaxNaps && !mbar_try_wait(bar0 + 8 * kQbQEmpty, (q_it & 1) ^ 1) && !*ctl.abort_flag; ++i)
+                    __nanosleep(kQ8Nap);
                 if (!wait_warp(bar0 + 8 * kQbQEmpty, (q_it & 1) ^ 1, ctl)) return;
                 if (!wait_warp(bar0 + 8 * kQbQSeen, (q_it & 1) ^ 1, ctl)) return;
                 ready = true;
@@ -325,7 +337,8 @@ __device__ void q8_split_q(const Q8Params& p, const int32_t* meta, uint8_t* smem
             }
         }
         fence_proxy_async_smem();
-        mbar_arrive(bar0 + 8 * kQbQFull);
+        __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive(bar0 + 8 * kQbQFull);
         ++q_it;
     }
 }
@@ -352,7 +365,7 @@ __device__ void q8_gemm1(const Q8Params& p, const int32_t* meta, uint8_t* smem, 
     WorkIter it;
     it.init(meta, p);
     Item item;
-    uint32_t s_it = 0, q_it = 0, slot = 0, phase = 0;
+    uint32_t s_it = 0, q_it = 0, slot = 0, phase = 0, rope = 0;
     bool ok = true;
     while (ok && it.next(p, item)) {
         ok = wait_warp(bar0 + 8 * kQbQFull, q_it & 1, ctl);
@@ -363,15 +376,24 @@ __device__ void q8_gemm1(const Q8Params& p, const int32_t* meta, uint8_t* smem, 
             if (!ok) break;
             const uint32_t d = tmem + C::kSCol + sb * C::kQN;
 #pragma unroll
-            for (int c = 0; c < kQ8Boxes; ++c) {
+            for (int hf = 0; hf < kQ8Halves; ++hf) {
                 ok = wait_warp(bar0 + 8 * (kQbFull0 + slot), phase, ctl);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t a_lo = (uint32_t)a0 + slot * (kQ8BoxBytes >> 4);
+                const uint32_t a_lo = (uint32_t)a0 + slot * (kQ8SlotBytes >> 4);
+                const uint32_t r_lo = (uint32_t)r0 + rope * (kQ8RopeBytes >> 4);
                 if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_f8(d, a_lo + 2 * k, a_hi, b_lo + (8 * c + 2 * k) * C::kQN, b_hi, kIdesc, c + k > 0);
+                    for (int k = 0; k < 8; ++k)
+                        umma_f8(d, a_lo + (k >> 2) * (kQ8BoxBytes >> 4) + 2 * (k & 3), a_hi, b_lo + (16 * hf + 2 * k) * C::kQN,
+                                b_hi, kIdesc, hf + k > 0);
+                    if (hf == kQ8Halves - 1) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            umma_f8(d, r_lo + 2 * k, r_hi, b_lo + (8 * kQ8Boxes + 2 * k) * C::kQN, b_hi, kIdesc, 1);
+                        umma_commit(bar0 + 8 * (kQbSFull0 + sb));
+                        if (j + 2 >= item.p1) umma_commit(bar0 + 8 * kQbQEmpty);
+                    }
                 }
                 __syncwarp();
                 if (++slot == C::kSlots) {
@@ -380,20 +402,7 @@ __device__ void q8_gemm1(const Q8Params& p, const int32_t* meta, uint8_t* smem, 
                 }
             }
             if (!ok) break;
-            const uint32_t rs = s_it % kQ8RopeSlots;
-            ok = wait_warp(bar0 + 8 * (kQbRopeFull0 + rs), (s_it / kQ8RopeSlots) & 1, ctl);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-                const uint32_t r_lo = (uint32_t)r0 + rs * (kQ8RopeBytes >> 4);
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    umma_f8(d, r_lo + 2 * k, r_hi, b_lo + (8 * kQ8Boxes + 2 * k) * C::kQN, b_hi, kIdesc, 1);
-                umma_commit(bar0 + 8 * (kQbRopeEmpty0 + rs));
-                umma_commit(bar0 + 8 * (kQbSFull0 + sb));
-                if (j + 2 >= item.p1) umma_commit(bar0 + 8 * kQbQEmpty);
-            }
-            __syncwarp();
+            if (++rope == C::kRopeSlots) rope = 0;
             ++s_it;
         }
         ++q_it;
@@ -428,15 +437,17 @@ __device__ void q8_gemm2(const Q8Params& p, const int32_t* meta, uint8_t* smem, 
             const uint32_t b_lo = (uint32_t)b0 + pb * (C::kPBytes >> 4);
             const uint32_t more = j == item.p0 ? 0u : 1u;
 #pragma unroll
-            for (int c = 0; c < kQ8Boxes; ++c) {
-                const uint32_t a_lo = (uint32_t)a0 + slot * (kQ8BoxBytes >> 4);
+            for (int hf = 0; hf < kQ8Halves; ++hf) {
+                const uint32_t a_lo = (uint32_t)a0 + slot * (kQ8SlotBytes >> 4);
                 if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kQ8Step / 32; ++k)
-                        umma_f8(tmem + C::kOCol + c * C::kNP, a_lo + k * (4096 >> 4), a_hi, b_lo + k * (512 >> 4), b_hi, kIdesc,
-                                k == 0 ? more : 1u);
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int k = 0; k < kQ8Step / 32; ++k)
+                            umma_f8(tmem + C::kOCol + (2 * hf + c) * C::kNP, a_lo + c * (kQ8BoxBytes >> 4) + k * (4096 >> 4), a_hi,
+                                    b_lo + k * (512 >> 4), b_hi, kIdesc, k == 0 ? more : 1u);
                     umma_commit(bar0 + 8 * (kQbEmpty0 + slot));
-                    if (c + 1 == kQ8Boxes) umma_commit(bar0 + 8 * (kQbPEmpty0 + pb));
+                    if (hf + 1 == kQ8Halves) umma_commit(bar0 + 8 * (kQbPEmpty0 + pb));
                 }
                 __syncwarp();
                 if (++slot == C::kSlots) slot = 0;
@@ -494,6 +505,10 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
     constexpr int kTermStride = NG * kQ8Step;
     uint8_t* pbase = smem + C::kPOff + cg * 16 * kQ8Step + row * 16;
     const bool causal2 = p.causal && p.s_q > 1;
+    auto arrive = [&](uint32_t bar) {  // once per warp, after all of its lanes
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
     WorkIter it;
     it.init(meta, p);
     Item item;
@@ -502,7 +517,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
     while (ok && it.next(p, item)) {
         ok = wait_warp(bar0 + 8 * kQbQFull, item_it & 1, ctl);
         if (!ok) break;
-        mbar_arrive(bar0 + 8 * kQbQSeen);
+        arrive(bar0 + 8 * kQbQSeen);
         const float4* qs4 = reinterpret_cast<const float4*>(qs_ring + (item_it & 1) * NG);
         const int gc0 = item.g * NG + cg * 16;  // first query column of the group
         // Table entries are fetched two steps ahead and page scales one, so
@@ -522,6 +537,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             l[c] = 0.f;
         }
         float R = fmaxf(sc0, sc1);
+        float bias = 0.f, back = 0.f, bias_ks = -1.f, bias_R = -1.f;
         for (int j = item.p0; j < item.p1; j += 2) {
             const float nx0 = page_scale(ph0), nx1 = page_scale(ph1);
             ph0 = entry(j + 4);
@@ -539,7 +555,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                 tmem_ld_x16(s + NG, lo);
                 tmem_ld_wait();
                 tc_fence_before();
-                mbar_arrive(bar0 + 8 * (kQbSEmpty0 + sb));
+                arrive(bar0 + 8 * (kQbSEmpty0 + sb));
 #pragma unroll
                 for (int c4 = 0; c4 < 4; ++c4) {
                     const float4 f = qs4[c4];
@@ -568,7 +584,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             const uint32_t gw = __any_sync(kFullMask, grow) ? 1u : 0u;
             if (lane == 0) vote[(s_it & 1) * 8 + wq] = gw;
             const uint32_t vbar = bar0 + 8 * (kQbVote0 + (s_it & 1) * 2 + cg);
-            mbar_arrive(vbar);
+            arrive(vbar);
             ok = wait_warp(vbar, (s_it >> 1) & 1, ctl);
             if (!ok) break;
             const uint4 v4 = *reinterpret_cast<const uint4*>(vote + (s_it & 1) * 8);
@@ -584,7 +600,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                     for (int c = 0; c < 16; ++c) zr[c] = z[c];
                     const float wmax = reduce16<true>(zr, lane);
                     if ((lane & 1) == 0) red[(lane >> 1) * 4 + wq] = wmax;
-                    mbar_arrive(bar0 + 8 * (kQbMax0 + cg));
+                    arrive(bar0 + 8 * (kQbMax0 + cg));
                     ok = wait_warp(bar0 + 8 * (kQbMax0 + cg), max_it & 1, ctl);
                     ++max_it;
                     if (!ok) break;
@@ -610,26 +626,29 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int i = 0; i < kQ8Boxes * kQ8Terms; i += 2) {
-                        float o[16], o1[16];
+                    for (int i = 0; i < kQ8Boxes * kQ8Terms; i += 3) {
+                        float o[3][16];
                         const uint32_t ta = tm + C::kOCol + i * NG + cg * 16;
-                        tmem_ld_x16(ta, o);
-                        tmem_ld_x16(ta + NG, o1);
+#pragma unroll
+                        for (int u = 0; u < 3; ++u) tmem_ld_x16(ta + u * NG, o[u]);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            o[c] *= alpha[c];
-                            o1[c] *= alpha[c];
+                        for (int u = 0; u < 3; ++u) {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) o[u][c] *= alpha[c];
+                            tmem_st_x16(ta + u * NG, o[u]);
                         }
-                        tmem_st_x16(ta, o);
-                        tmem_st_x16(ta + NG, o1);
                     }
                     tmem_st_wait();
                 }
             }
-            const float bias = kQ8Bias + __log2f(ks / R);
+            if (ks != bias_ks || R != bias_R) {  // (page scales seldom differ, and the largest seldom grows)
+                bias_ks = ks;
+                bias_R = R;
+                bias = kQ8Bias + __log2f(ks / R);
+                back = exp2f(-bias);  // x -> p
+            }
             if (bias > kQ8MinBias) {
-                const float back = exp2f(-bias);  // x -> p
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
                     z[c] = ex2_approx(z[c] - m[c] + bias);
@@ -657,8 +676,9 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                 if (cg == 0) {
 #pragma unroll 1
                     for (int c = 0; c < kQ8Boxes; ++c) {
-                        const uint32_t slot = (s_it * kQ8Boxes + c) % C::kSlots;
-                        uint4* d = reinterpret_cast<uint4*>(smem + C::kBoxOff + slot * kQ8BoxBytes + row * 128);
+                        const uint32_t slot = (s_it * kQ8Halves + (c >> 1)) % C::kSlots;
+                        uint4* d = reinterpret_cast<uint4*>(smem + C::kBoxOff + slot * kQ8SlotBytes +
+                                                            (c & 1) * kQ8BoxBytes + row * 128);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) d[i] = make_uint4(0, 0, 0, 0);
                     }
@@ -666,7 +686,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             }
             fence_proxy_async_smem();
             tc_fence_before();
-            mbar_arrive(bar0 + 8 * (kQbPFull0 + pb));
+            arrive(bar0 + 8 * (kQbPFull0 + pb));
             sc0 = nx0;
             sc1 = nx1;
             ++s_it;
@@ -678,7 +698,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             const float wsum = reduce16<false>(l, lane);
             if ((lane & 1) == 0) sums[(lane >> 1) * 4 + wq] = wsum;
         }
-        mbar_arrive(bar0 + 8 * (kQbSum0 + cg));
+        arrive(bar0 + 8 * (kQbSum0 + cg));
         ok = wait_warp(bar0 + 8 * (kQbSum0 + cg), item_it & 1, ctl);
         if (!ok) break;
         const uint32_t last = s_it - 1;
@@ -729,7 +749,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
         }
         if (!item.unsplit && item.slot < 0 && row == 0) atomicOr(p.status, MLA_STATUS_BAD_SCHEDULE);
         tc_fence_before();
-        mbar_arrive(bar0 + 8 * kQbOEmpty);
+        arrive(bar0 + 8 * kQbOEmpty);
         ++item_it;
     }
 }
@@ -750,13 +770,13 @@ __global__ void __launch_bounds__(Q8Cfg<NG>::kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
     int32_t* meta_s = reinterpret_cast<int32_t*>(smem + C::kPlanMetaOff);
-    constexpr int kSm = 128 * C::kColGroups;  // softmax threads
+    constexpr int kSm = 4 * C::kColGroups;  // softmax warps (a warp arrives once)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kQbCount; ++i) {
             uint32_t count = 1;
             if (i == kQbSEmpty0 || i == kQbSEmpty1 || i == kQbPFull0 || i == kQbPFull1 || i == kQbOEmpty || i == kQbQSeen)
                 count = kSm;
-            if ((i >= kQbVote0 && i < kQbRopeFull0) || i == kQbQFull) count = 128;
+            if ((i >= kQbVote0 && i < kQbFull0) || i == kQbQFull) count = 4;
             mbar_init(bar0 + 8 * i, count);
         }
         *abort_flag = 0;
@@ -773,7 +793,7 @@ __global__ void __launch_bounds__(Q8Cfg<NG>::kThreads, 1)
     tc_fence_after();
     // The plan from the lengths, and the first step's pages, before the wait on
     // the grid before this one (see mla_decode_fwd_kernel).
-    int32_t* plan_scratch = reinterpret_cast<int32_t*>(smem + C::kBoxOff + kQ8Boxes * kQ8BoxBytes);
+    int32_t* plan_scratch = reinterpret_cast<int32_t*>(smem + C::kBoxOff + kQ8Halves * kQ8SlotBytes);
     bool first_issued = false;
     if (p.plan_out != nullptr) {
         build_plan_in_cta(p, plan_scratch, meta_s);
@@ -788,11 +808,7 @@ __global__ void __launch_bounds__(Q8Cfg<NG>::kThreads, 1)
                 if ((unsigned)ph0 < (unsigned)p.num_blocks &&
                     (item.p0 + 1 >= item.p1 || (unsigned)ph1 < (unsigned)p.num_blocks)) {
                     const uint64_t policy = p.share > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
-                    for (int c = 0; c < kQ8Boxes; ++c)
-                        q8_load(&kv_map, &rope_map, smem_addr(smem + C::kBoxOff) + c * kQ8BoxBytes, bar0 + 8 * (kQbFull0 + c),
-                                c, ph0, ph1, policy);
-                    q8_load(&kv_map, &rope_map, smem_addr(smem + C::kRopeOff), bar0 + 8 * kQbRopeFull0, kQ8Boxes, ph0, ph1,
-                            policy);
+                    for (int hf = 0; hf < kQ8Halves; ++hf) q8_load<NG>(&kv_map, &rope_map, smem, hf, 0, hf, ph0, ph1, policy);
                     first_issued = true;
                 }
             }
@@ -819,18 +835,23 @@ __global__ void __launch_bounds__(Q8Cfg<NG>::kThreads, 1)
         meta = hdr + kHdrWords + (size_t)(blockIdx.x / p.share) * kMetaWords;
     }
     const Ctl ctl{abort_flag, p.status};
-    if (warp == 0) {
-        if (lane == 0) q8_producer<NG>(&kv_map, &rope_map, p, meta, smem, ctl, first_issued);
-    } else if (warp == 1) {
-        q8_gemm1<NG>(p, meta, smem, tmem, ctl);
-        q8_drain(bar0 + 8 * kQbDone1);
-    } else if (warp == 2) {
-        q8_gemm2<NG>(p, meta, smem, tmem, ctl);
-        q8_drain(bar0 + 8 * kQbDone2);
-    } else if (warp >= C::kFirstSoftmax) {
+    if (warp >= C::kFirstSoftmax) {
+        if constexpr (C::kSplitRegs) setmaxnreg_inc<C::kRegsSoftmax>();
         q8_softmax<NG>(p, meta, smem, tmem, ctl);
     } else if (warp >= C::kFirstQ) {
+        if constexpr (C::kSplitRegs) setmaxnreg_dec<C::kRegsQ>();
         q8_split_q<NG>(p, meta, smem, ctl);
+    } else {
+        if constexpr (C::kSplitRegs) setmaxnreg_dec<C::kRegsIssue>();
+        if (warp == 0) {
+            if (lane == 0) q8_producer<NG>(&kv_map, &rope_map, p, meta, smem, ctl, first_issued);
+        } else if (warp == 1) {
+            q8_gemm1<NG>(p, meta, smem, tmem, ctl);
+            q8_drain(bar0 + 8 * kQbDone1);
+        } else if (warp == 2) {
+            q8_gemm2<NG>(p, meta, smem, tmem, ctl);
+            q8_drain(bar0 + 8 * kQbDone2);
+        }
     }
     tc_fence_before();
     __syncthreads();
