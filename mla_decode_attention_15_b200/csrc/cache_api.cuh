@@ -284,7 +284,7 @@ int mla_rope_init(const mla_rope_config* c, mla_rope_table* t) {
 int mla_rope_apply(const mla_rope_dims* d, const mla_rope_table* table, const void* x, const int32_t* positions, void* out,
                    void* stream) {
     if (d == nullptr || table == nullptr) return MLA_ERR_INVALID_ARG;
-    if (d->tokens < 0 || d->num_heads < 1 || d->width < 2 * kRopePairs || d->width > 65536 || d->width % 8 != 0 ||
+    if (d->tokens < 0 || d->num_heads < 1 || d->width < 2 * kRopePairs || d->width > 2048 || d->width % 8 != 0 ||
         d->offset < 0 || d->offset % 8 != 0 || d->offset + 2 * kRopePairs > d->width ||
         (d->transpose != 0 && d->transpose != 1))
         return MLA_ERR_INVALID_ARG;

@@ -86,9 +86,9 @@ struct RopeParams {
     const int32_t* positions;
     void* out;
     int64_t xt, xh, ot, oh;  // strides in values
-    int T, h, width, offset, transpose;
+    int T, h, offset, transpose;
     int tpc, hpc;            // tokens and heads per CTA
-    int in_place;
+    int per_row, rows_pass;  // units per row, rows per pass of the CTA's threads
     mla_rope_table table;
 };
 
@@ -124,79 +124,83 @@ struct Chunk8<float> {
     }
 };
 
-// A CTA takes tpc tokens x hpc heads.  The angles of its tokens are computed
-// once, in shared memory, and serve every head; then each thread takes units of
-// 8 columns (16 in the half layout's rotary part, whose pairs lie 32 columns
-// apart), kRopeUnroll of them in flight.  Bound by the bytes of x and out; the
-// small calls by the launch.
-constexpr int kRopeUnroll = 4;
+// A CTA takes tpc tokens x hpc heads.  A thread owns one unit of a row (8 columns; in
+// the half layout's rotary part 16, whose pairs lie 32 columns apart) and walks
+// the rows with it, kRopeUnroll of them in flight, so that nothing is divided per
+// unit.  The first rows are on their way while the angles of the CTA's
+// tokens are computed, once, into shared memory for every head.  Bound by the
+// bytes of x and out; small calls by the launch.  B200, 4099 tokens x 128 heads x 192
+// bf16 columns (403 MB, 61.5 us at the copy rate), half layout: 111 us with a division
+// per unit and the angles first; 97 us without, 4 rows in flight per thread and 3 CTAs
+// per SM; 84 us with 4 CTAs; 76.3 us with 2 rows and 6 CTAs, as it is (1 row and
+// 8 CTAs 78.2, 2 and 8 84.4; 64 or 256 instead of 128 rows per CTA 77.9 and 92.1).
+constexpr int kRopeUnroll = 2;
 constexpr int kRopeMaxTokens = 16;
 template <typename E, bool kInterleaved>
-__global__ void __launch_bounds__(kMoveThreads) mla_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kMoveThreads, sizeof(E) == 2 ? 6 : 4) mla_rope_kernel(const __grid_constant__ RopeParams p) {
     __shared__ float2 cs[kRopeMaxTokens][kRopePairs];
+    constexpr int kRot = kInterleaved ? 8 : 4;  // units of the rotary part
     const int t0 = blockIdx.x * p.tpc, h0 = blockIdx.y * p.hpc;
     const int nt = min(p.tpc, p.T - t0), nh = min(p.hpc, p.h - h0);
-    for (int i = threadIdx.x; i < nt * kRopePairs; i += kMoveThreads) {
-        const int t = i / kRopePairs, k = i % kRopePairs;
-        float2 v = rope_cos_sin(p.table.turns, p.table.amplitude, p.positions[t0 + t], k);
-        if (p.transpose) v.y = -v.y;
-        cs[t][k] = v;
-    }
-    __syncthreads();
-    constexpr int kRot = kInterleaved ? 8 : 4;  // units of the rotary part
-    const int rest = p.in_place ? 0 : (p.width - 2 * kRopePairs) / 8;
-    const int per_row = kRot + rest;
-    const int total = nt * nh * per_row;
+    const int rows = nt * nh;
+    const int r0 = threadIdx.x / p.per_row, u = threadIdx.x - r0 * p.per_row;
+    const bool rot = u < kRot;
+    // rotary units first, then the columns around them
     const int off8 = p.offset / 8;
-    const E* x = static_cast<const E*>(p.x);
-    E* out = static_cast<E*>(p.out);
-    for (int base = threadIdx.x; base < total; base += kMoveThreads * kRopeUnroll) {
-        Chunk8<E> v[kRopeUnroll], v2[kInterleaved ? 1 : kRopeUnroll];
-        int64_t to[kRopeUnroll];
-        int unit[kRopeUnroll], tok[kRopeUnroll];
+    const int col = 8 * (rot ? off8 + u : u - kRot < off8 ? u - kRot : u - kRot + 8);
+    const E* x = static_cast<const E*>(p.x) + (int64_t)t0 * p.xt + (int64_t)h0 * p.xh + col;
+    E* out = static_cast<E*>(p.out) + (int64_t)t0 * p.ot + (int64_t)h0 * p.oh + col;
+    const int mine = r0 < p.rows_pass ? rows : 0;  // (the last threads of the block may own no unit)
+    Chunk8<E> v[kRopeUnroll], v2[kInterleaved ? 1 : kRopeUnroll];
+    auto load = [&](int base) {
 #pragma unroll
         for (int i = 0; i < kRopeUnroll; ++i) {
-            const int w = base + i * kMoveThreads;
-            unit[i] = -1;
-            if (w < total) {
-                const int row = w / per_row, u = w - row * per_row;
-                const int t = row / nh, hd = row - t * nh;
-                unit[i] = u;
-                tok[i] = t;
-                // rotary units first, then the columns around them
-                int c = u - kRot;
-                c = u < kRot ? off8 + u : c < off8 ? c : c + 8;
-                const E* s = x + (int64_t)(t0 + t) * p.xt + (int64_t)(h0 + hd) * p.xh + c * 8;
-                to[i] = (int64_t)(t0 + t) * p.ot + (int64_t)(h0 + hd) * p.oh + c * 8;
+            const int row = base + r0 + i * p.rows_pass;
+            if (row < mine) {
+                const int t = p.tpc == 1 ? 0 : row / nh;
+                const E* s = x + t * p.xt + (row - t * nh) * p.xh;
                 v[i].load(s);
                 if constexpr (!kInterleaved)
-                    if (u < kRot) v2[i].load(s + kRopePairs);
+                    if (rot) v2[i].load(s + kRopePairs);
             }
         }
+    };
+    load(0);
+    for (int i = threadIdx.x; i < nt * kRopePairs; i += blockDim.x) {
+        const int t = i / kRopePairs, k = i % kRopePairs;
+        float2 c = rope_cos_sin(p.table.turns, p.table.amplitude, p.positions[t0 + t], k);
+        if (p.transpose) c.y = -c.y;
+        cs[t][k] = c;
+    }
+    __syncthreads();
+    for (int base = 0; base < rows; base += kRopeUnroll * p.rows_pass) {
+        if (base > 0) load(base);
 #pragma unroll
         for (int i = 0; i < kRopeUnroll; ++i) {
-            if (unit[i] < 0) continue;
-            if (unit[i] < kRot) {
-                const float2* c = cs[tok[i]];
+            const int row = base + r0 + i * p.rows_pass;
+            if (row >= mine) continue;
+            const int t = p.tpc == 1 ? 0 : row / nh;
+            E* d = out + t * p.ot + (row - t * nh) * p.oh;
+            if (rot) {
+                const float2* c = cs[t] + u * (kInterleaved ? 4 : 8);
                 float a[8];
                 v[i].get(a);
                 if constexpr (kInterleaved) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) rotate(a[2 * k], a[2 * k + 1], c[unit[i] * 4 + k]);
+                    for (int k = 0; k < 4; ++k) rotate(a[2 * k], a[2 * k + 1], c[k]);
                 } else {
                     float b[8];
                     v2[i].get(b);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) rotate(a[k], b[k], c[unit[i] * 8 + k]);
+                    for (int k = 0; k < 8; ++k) rotate(a[k], b[k], c[k]);
                     v2[i].set(b);
-                    v2[i].store(out + to[i] + kRopePairs);
+                    v2[i].store(d + kRopePairs);
                 }
                 v[i].set(a);
             }
-            v[i].store(out + to[i]);
+            v[i].store(d);
         }
     }
-    __threadfence();
 }
 
 inline bool launch_rope(const mla_rope_dims& d, const mla_rope_table& table, const void* x, const int32_t* positions, void* out,
@@ -211,25 +215,29 @@ inline bool launch_rope(const mla_rope_dims& d, const mla_rope_table& table, con
     p.oh = d.out_head_stride;
     p.T = d.tokens;
     p.h = d.num_heads;
-    p.width = d.width;
     p.offset = d.offset;
     p.transpose = d.transpose;
-    p.in_place = x == out;
     p.table = table;
-    // About kMoveThreads * kRopeUnroll units per CTA: several heads of a token,
-    // or several tokens where there are few heads.
-    const int per_row = (p.in_place ? 0 : (d.width - 2 * kRopePairs) / 8) + (table.interleaved ? 8 : 4);
-    const int rows = max(1, kMoveThreads * kRopeUnroll / per_row);
-    p.hpc = min(d.num_heads, rows);
-    p.tpc = min(min(kRopeMaxTokens, d.tokens), max(1, rows / p.hpc));
+    // units per row (at most kMoveThreads: rows are at most 2048 values wide), and
+    // rows that one pass of the CTA's threads covers
+    p.per_row = (table.interleaved ? 8 : 4) + (x == out ? 0 : (d.width - 2 * kRopePairs) / 8);
+    p.rows_pass = kMoveThreads / p.per_row;
+    // Enough rows per CTA for a few rounds of loads (the angles are computed once for
+    // all of them), but no fewer CTAs than fill the device.
+    const int64_t all = (int64_t)d.tokens * d.num_heads;
+    const int64_t share = all / (2 * 148) > 1 ? all / (2 * 148) : 1;
+    const int want = (int)min((int64_t)128, max((int64_t)p.rows_pass, share));
+    p.hpc = min(d.num_heads, want);
+    p.tpc = min(min(kRopeMaxTokens, d.tokens), max(1, want / p.hpc));
     const dim3 grid((d.tokens + p.tpc - 1) / p.tpc, (d.num_heads + p.hpc - 1) / p.hpc);
     if (grid.y > 65535) return false;
+    const int threads = (p.rows_pass * p.per_row + 31) / 32 * 32;
     if (d.dtype == MLA_DTYPE_BF16) {
-        if (table.interleaved) mla_rope_kernel<__nv_bfloat16, true><<<grid, kMoveThreads, 0, stream>>>(p);
-        else mla_rope_kernel<__nv_bfloat16, false><<<grid, kMoveThreads, 0, stream>>>(p);
+        if (table.interleaved) mla_rope_kernel<__nv_bfloat16, true><<<grid, threads, 0, stream>>>(p);
+        else mla_rope_kernel<__nv_bfloat16, false><<<grid, threads, 0, stream>>>(p);
     } else {
-        if (table.interleaved) mla_rope_kernel<float, true><<<grid, kMoveThreads, 0, stream>>>(p);
-        else mla_rope_kernel<float, false><<<grid, kMoveThreads, 0, stream>>>(p);
+        if (table.interleaved) mla_rope_kernel<float, true><<<grid, threads, 0, stream>>>(p);
+        else mla_rope_kernel<float, false><<<grid, threads, 0, stream>>>(p);
     }
     return true;
 }
@@ -328,19 +336,22 @@ __device__ __forceinline__ uint32_t amax_of(uint32_t amax, float x) {
     return b < kInfBits ? max(amax, b) : amax;
 }
 
-// One CTA per touched page: it holds the page's new rows in registers (16 pieces of
-// 8 latent columns and 2 of 4 RoPE pairs per thread for a full page), so the scale
-// costs no second read of them.  The CTA finds its (request, page) by a scan over the
-// requests' page counts.
+// One CTA per touched page: it holds the page's new rows in registers (per thread
+// kLatRows pieces of 8 latent columns and 4 RoPE pairs for a full page; two such CTAs
+// fit an SM), so the scale costs no second read of them.  The CTA finds its
+// (request, page) by a scan over the requests' page counts.
+constexpr int kAppendThreads = 512;
+constexpr int kLatRows = kPage * (kDv / 8) / kAppendThreads;  // 8
+static_assert(kPage * 8 == kAppendThreads, "one RoPE unit per thread");
 template <bool kQ8>
-__global__ void __launch_bounds__(kMoveThreads) mla_cache_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 2) mla_cache_append_kernel(const __grid_constant__ AppendParams p) {
     __shared__ int tot[33];
     __shared__ int job[4];  // request, page within its new pages
-    __shared__ uint32_t warp_max[kMoveThreads / 32];
+    __shared__ uint32_t warp_max[kAppendThreads / 32];
     const int tid = threadIdx.x;
     if (tid == 0) job[0] = -1;
     int before = 0;
-    for (int base = 0; base < p.batch; base += kMoveThreads) {
+    for (int base = 0; base < p.batch; base += kAppendThreads) {
         const int b = base + tid;
         bool bad = false;
         int pages = 0;
@@ -371,21 +382,19 @@ __global__ void __launch_bounds__(kMoveThreads) mla_cache_append_kernel(const __
     const int64_t src0 = (int64_t)nr.first + (page * kPage - nr.start);  // source row of page row 0
     uint8_t* dst = p.pool.kv + (size_t)phys * p.pool.page_bytes;
 
-    // latent: piece tid % 64 of rows r0 + tid / 64 + 4 k;  RoPE: unit tid % 8 of rows r0 + tid / 8 + 32 k
+    // latent: piece tid % 64 of rows r0 + tid / 64 + 8 k;  RoPE: unit tid % 8 of row r0 + tid / 8
     const int lc = tid & 63, lr = tid >> 6, pu = tid & 7, pr = tid >> 3;
-    uint4 lat[16];
-    float pe[2][8];
+    uint4 lat[kLatRows];
+    float pe[8];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-        const int r = r0 + lr + 4 * k;
+    for (int k = 0; k < kLatRows; ++k) {
+        const int r = r0 + lr + 8 * k;
         if (r < r1) lat[k] = *reinterpret_cast<const uint4*>(p.c_kv + (src0 + r) * p.c_stride + lc * 8);
     }
     const bool inter = !p.rotate || p.rope.interleaved;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int r = r0 + pr + 32 * k;
-        if (r >= r1) continue;
-        const __nv_bfloat16* s = p.k_pe + (src0 + r) * p.pe_stride;
+    const int rr = r0 + pr;
+    if (rr < r1) {
+        const __nv_bfloat16* s = p.k_pe + (src0 + rr) * p.pe_stride;
         uint4 raw;
         if (inter) {
             raw = *reinterpret_cast<const uint4*>(s + pu * 8);
@@ -394,47 +403,63 @@ __global__ void __launch_bounds__(kMoveThreads) mla_cache_append_kernel(const __
             const uint2 hi = *reinterpret_cast<const uint2*>(s + kRopePairs + pu * 4);
             raw = make_uint4(lo.x, lo.y, hi.x, hi.y);
         }
-        unpack8(raw, pe[k]);
+        unpack8(raw, pe);
         if (p.rotate) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 c = rope_cos_sin(p.rope.turns, p.rope.amplitude, page * kPage + r, pu * 4 + i);
+                const float2 c = rope_cos_sin(p.rope.turns, p.rope.amplitude, page * kPage + rr, pu * 4 + i);
                 // (selected, not indexed: both layouts keep the values in registers)
-                float a = inter ? pe[k][2 * i] : pe[k][i], z = inter ? pe[k][2 * i + 1] : pe[k][i + 4];
+                float a = inter ? pe[2 * i] : pe[i], z = inter ? pe[2 * i + 1] : pe[i + 4];
                 rotate(a, z, c);
                 if (inter) {
-                    pe[k][2 * i] = a;
-                    pe[k][2 * i + 1] = z;
+                    pe[2 * i] = a;
+                    pe[2 * i + 1] = z;
                 } else {
-                    pe[k][i] = a;
-                    pe[k][i + 4] = z;
+                    pe[i] = a;
+                    pe[i + 4] = z;
                 }
             }
         }
     }
     float inv = 1.f;
     if constexpr (kQ8) {
-        uint32_t amax = 0;
+        // Largest magnitude as bits, non-finite values included: they are the
+        // largest, and where there is none the finite maximum is at hand.
+        uint32_t top = 0;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            if (r0 + lr + 4 * k >= r1) continue;
-            float f[8];
-            unpack8(lat[k], f);
+        for (int k = 0; k < kLatRows; ++k) {
+            if (r0 + lr + 8 * k >= r1) continue;
+            const uint32_t w[4] = {lat[k].x, lat[k].y, lat[k].z, lat[k].w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) amax = amax_of(amax, f[i]);
+            for (int i = 0; i < 4; ++i) top = max(top, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
         }
+        if (rr < r1)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (r0 + pr + 32 * k >= r1) continue;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) amax = amax_of(amax, pe[k][i]);
-        }
-        amax = __reduce_max_sync(0xffffffffu, amax);
-        if ((tid & 31) == 0) warp_max[tid >> 5] = amax;
+            for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(pe[i]) & 0x7fffffffu);
+        top = __reduce_max_sync(0xffffffffu, top);
+        if ((tid & 31) == 0) warp_max[tid >> 5] = top;
         const float held = r0 > 0 ? p.pool.scales[phys] : 0.f;  // (read by all before thread 0 writes it)
         __syncthreads();
+        uint32_t amax = 0;
 #pragma unroll
-        for (int w = 0; w < kMoveThreads / 32; ++w) amax = max(amax, warp_max[w]);
+        for (int w = 0; w < kAppendThreads / 32; ++w) amax = max(amax, warp_max[w]);
+        if (amax >= kInfBits) {  // (seldom: some value is not finite)
+            uint32_t fin = 0;
+            for (int k = 0; k < kLatRows; ++k) {
+                if (r0 + lr + 8 * k >= r1) continue;
+                float f[8];
+                unpack8(lat[k], f);
+                for (int i = 0; i < 8; ++i) fin = amax_of(fin, f[i]);
+            }
+            if (rr < r1)
+                for (int i = 0; i < 8; ++i) fin = amax_of(fin, pe[i]);
+            fin = __reduce_max_sync(0xffffffffu, fin);
+            __syncthreads();
+            if ((tid & 31) == 0) warp_max[tid >> 5] = fin;
+            __syncthreads();
+            amax = 0;
+            for (int w = 0; w < kAppendThreads / 32; ++w) amax = max(amax, warp_max[w]);
+        }
         const int e = amax == 0 ? kMinScaleExp : min(max(e4m3_scale_exp(amax), kMinScaleExp), kMaxScaleExp);
         const float scale = fmaxf(pow2f(e), held);
         inv = 1.f / scale;
@@ -442,7 +467,7 @@ __global__ void __launch_bounds__(kMoveThreads) mla_cache_append_kernel(const __
             // The page's earlier rows move to the larger scale.
             const float f = held / scale;
             uint2* rows = reinterpret_cast<uint2*>(dst);
-            for (int i = tid; i < r0 * (kDqk / 8); i += kMoveThreads) {
+            for (int i = tid; i < r0 * (kDqk / 8); i += kAppendThreads) {
                 const uint2 v = rows[i];
                 const uint32_t w[4] = {v.x & 0xffffu, v.x >> 16, v.y & 0xffffu, v.y >> 16};
                 uint32_t o[4];
@@ -457,8 +482,8 @@ __global__ void __launch_bounds__(kMoveThreads) mla_cache_append_kernel(const __
         if (tid == 0) p.pool.scales[phys] = scale;
     }
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-        const int r = r0 + lr + 4 * k;
+    for (int k = 0; k < kLatRows; ++k) {
+        const int r = r0 + lr + 8 * k;
         if (r >= r1) continue;
         if constexpr (kQ8) {
             float f[8];
@@ -468,13 +493,10 @@ __global__ void __launch_bounds__(kMoveThreads) mla_cache_append_kernel(const __
             *reinterpret_cast<uint4*>(dst + (r * kDqk + lc * 8) * 2) = lat[k];
         }
     }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int r = r0 + pr + 32 * k;
-        if (r >= r1) continue;
+    if (rr < r1) {
         if constexpr (kQ8) {
-            const uint2 v = quant8(pe[k], inv);
-            uint8_t* d = dst + r * kDqk + kDv;
+            const uint2 v = quant8(pe, inv);
+            uint8_t* d = dst + rr * kDqk + kDv;
             if (inter) {
                 *reinterpret_cast<uint2*>(d + pu * 8) = v;
             } else {
@@ -482,8 +504,8 @@ __global__ void __launch_bounds__(kMoveThreads) mla_cache_append_kernel(const __
                 *reinterpret_cast<uint32_t*>(d + kRopePairs + pu * 4) = v.y;
             }
         } else {
-            const uint4 v = pack8(pe[k]);
-            __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(dst) + r * kDqk + kDv;
+            const uint4 v = pack8(pe);
+            __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(dst) + rr * kDqk + kDv;
             if (inter) {
                 *reinterpret_cast<uint4*>(d + pu * 8) = v;
             } else {
@@ -498,8 +520,8 @@ __global__ void __launch_bounds__(kMoveThreads) mla_cache_append_kernel(const __
 inline void launch_append(const AppendParams& p, cudaStream_t stream) {
     // n new rows touch at most n pages, and at most n / 64 + 2
     const int64_t most = min((int64_t)p.tokens, (int64_t)p.tokens / kPage + 2 * (int64_t)p.batch);
-    if (p.pool.scales != nullptr) mla_cache_append_kernel<true><<<(unsigned)most, kMoveThreads, 0, stream>>>(p);
-    else mla_cache_append_kernel<false><<<(unsigned)most, kMoveThreads, 0, stream>>>(p);
+    if (p.pool.scales != nullptr) mla_cache_append_kernel<true><<<(unsigned)most, kAppendThreads, 0, stream>>>(p);
+    else mla_cache_append_kernel<false><<<(unsigned)most, kAppendThreads, 0, stream>>>(p);
 }
 
 // ------------------------------------------------------------------ page moves
@@ -534,6 +556,22 @@ inline void launch_copy_pages(const CachePool& pool, int n, const int32_t* src, 
     mla_cache_copy_kernel<<<dim3(n, page_slices(pool.page_bytes)), kMoveThreads, 0, stream>>>(pool, src, dst, status);
 }
 
+// The second kernel of a call, launched as a programmatic dependent of the first: its
+// launch overlaps the first one's run.
+template <typename... P, typename... A>
+inline void launch_after(void (*kernel)(P...), dim3 grid, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);  // (an error is the caller's to collect)
+}
+
 // ------------------------------------------------------------------ fork
 constexpr int kForkMax = 1024;
 constexpr int kBookThreads = 1024;
@@ -546,16 +584,26 @@ __host__ __device__ inline size_t fork_workspace_words(int n) { return (size_t)k
 // a page and hands them the lowest free ones.
 __global__ void __launch_bounds__(kBookThreads)
     mla_cache_fork_plan_kernel(const CacheBooks k, int n, const int32_t* parents, const int32_t* children, int32_t* ws) {
-    __shared__ int child_s[kForkMax];
+    __shared__ __align__(16) int child_s[kForkMax];
     __shared__ int fresh[kForkMax];
     __shared__ int tot[33];
+    griddep_launch_dependents();  // (the copies wait for this grid's end)
     const int i = threadIdx.x;
     const int parent = i < n ? parents[i] : -1, child = i < n ? children[i] : -1;
-    if (i < n) child_s[i] = child;
+    child_s[i] = i < n ? child : -1;  // (kForkMax threads)
     __syncthreads();
     bool ok = i < n && (unsigned)parent < (unsigned)k.batch && (unsigned)child < (unsigned)k.batch;
-    if (ok)
-        for (int j = 0; j < i; ++j) ok &= child_s[j] != child;
+    if (ok) {  // not named before: four rows at a time
+        bool again = false;
+        const int4* c4 = reinterpret_cast<const int4*>(child_s);
+#pragma unroll 4
+        for (int j = 0; j < i / 4; ++j) {
+            const int4 c = c4[j];
+            again |= c.x == child || c.y == child || c.z == child || c.w == child;
+        }
+        for (int j = i & ~3; j < i; ++j) again |= child_s[j] == child;
+        ok = !again;
+    }
     int L = 0;
     if (ok) {
         L = k.lens[parent];
@@ -622,6 +670,7 @@ __global__ void __launch_bounds__(kBookThreads)
 __global__ void __launch_bounds__(kMoveThreads)
     mla_cache_fork_kernel(const CacheBooks k, const CachePool pool, const int32_t* parents, const int32_t* children,
                           const int32_t* ws) {
+    griddep_wait();  // the plan
     const int32_t* w = ws + kForkWords * blockIdx.x;
     if (!w[kForkOk]) return;
     if (blockIdx.y + 1 < gridDim.y) {
@@ -641,7 +690,8 @@ __global__ void __launch_bounds__(kMoveThreads)
 inline void launch_fork(const CacheBooks& k, const CachePool& pool, int n, const int32_t* parents, const int32_t* children,
                         int32_t* ws, cudaStream_t stream) {
     mla_cache_fork_plan_kernel<<<1, kBookThreads, 0, stream>>>(k, n, parents, children, ws);
-    mla_cache_fork_kernel<<<dim3(n, page_slices(pool.page_bytes) + 1), kMoveThreads, 0, stream>>>(k, pool, parents, children, ws);
+    launch_after(mla_cache_fork_kernel, dim3(n, page_slices(pool.page_bytes) + 1), stream, k, pool, parents, children,
+                 (const int32_t*)ws);
 }
 
 // ------------------------------------------------------------------ free
@@ -682,37 +732,69 @@ inline size_t compact_workspace_words(int num_blocks) { return kCompactList + 2 
 
 // As many free pages lie before `live` as pages in use behind it (live counts
 // both those in use before it and those behind), so one running count over the
-// pages that move or are moved to numbers both lists.
+// pages that move or are moved to numbers both lists.  A warp owns a run of
+// consecutive pages, 32 at a time, and a lane keeps which of its pages are in use as
+// bits, so the counts are read once up to 65,536 pages (again for more), and
+// only the warps' totals meet across the block.
+constexpr int kPlanBits = 64;
 __global__ void __launch_bounds__(kBookThreads) mla_cache_compact_plan_kernel(const CacheBooks k, int32_t* ws) {
     __shared__ int tot[33];
-    const int nb = k.num_blocks, i = threadIdx.x;
+    griddep_launch_dependents();  // (the moves wait for this grid's end)
+    const int nb = k.num_blocks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int span = kBookThreads * kPlanBits;
+    // pages per lane and round, in eights: eight loads are in flight at a time
+    const int per = nb < span ? ((nb + kBookThreads - 1) / kBookThreads + 7) / 8 * 8 : kPlanBits;
+    auto in_use = [&](int base) -> uint64_t {
+        const int first = base + warp * 32 * per + lane;
+        uint64_t bits = 0;
+        for (int u = 0; u < per; u += 8) {
+            int v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = first + 32 * (u + i) < nb ? k.refs[first + 32 * (u + i)] : 0;
+            uint32_t b = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) b |= (v[i] > 0 ? 1u : 0u) << i;
+            bits |= (uint64_t)b << u;
+        }
+        return bits;
+    };
     int mine = 0;
-    for (int page = i; page < nb; page += kBookThreads) mine += k.refs[page] > 0;
+    uint64_t bits = 0;
+    for (int base = 0; base < nb; base += kBookThreads * per) {
+        bits = in_use(base);
+        mine += __popcll(bits);
+    }
     int live;
     block_exclusive(mine, tot, &live);
     int32_t* list = ws + kCompactList;
     int32_t* place = list + nb;
     int before = 0;
-    for (int base = 0; base < nb; base += kBookThreads * kBookUnroll) {
-        int at[kBookUnroll], cnt = 0;
-#pragma unroll
-        for (int u = 0; u < kBookUnroll; ++u) {
-            const int page = base + i * kBookUnroll + u;
-            at[u] = page < nb && (k.refs[page] > 0) == (page >= live) ? 1 : 0;
-            cnt += at[u];
+    for (int base = 0; base < nb; base += kBookThreads * per) {
+        if (nb > kBookThreads * per) bits = in_use(base);
+        const int first = base + warp * 32 * per + lane;
+        // pages that move or are moved to
+        uint64_t at = 0;
+#pragma unroll 8
+        for (int u = 0; u < per; ++u) {
+            const int page = first + 32 * u;
+            if (page < nb && (bool)((bits >> u) & 1) == (page >= live)) at |= 1ull << u;
         }
         int total;
-        int r = before + block_exclusive(cnt, tot, &total);
-#pragma unroll
-        for (int u = 0; u < kBookUnroll; ++u) {
-            const int page = base + i * kBookUnroll + u;
-            if (at[u]) list[r] = page;
-            if (page < nb && page >= live) place[page] = at[u] ? r : -1;
-            r += at[u];
+        const int r = before + block_exclusive(__popcll(at), tot, &total);
+        int run = __shfl_sync(0xffffffffu, r, 0);  // of the warp's first page
+#pragma unroll 8
+        for (int u = 0; u < per; ++u) {
+            const int page = first + 32 * u;
+            const bool hit = (at >> u) & 1;
+            const unsigned hits = __ballot_sync(0xffffffffu, hit);
+            const int rank = run + __popc(hits & ((1u << lane) - 1));
+            if (hit) list[rank] = page;
+            if (page < nb && page >= live) place[page] = hit ? rank : -1;
+            run += __popc(hits);
         }
         before += total;
     }
-    if (i == 0) {
+    if (threadIdx.x == 0) {
         ws[kCompactLive] = live;
         ws[kCompactMoves] = before / 2;
     }
@@ -720,6 +802,7 @@ __global__ void __launch_bounds__(kBookThreads) mla_cache_compact_plan_kernel(co
 
 __global__ void __launch_bounds__(kMoveThreads)
     mla_cache_compact_kernel(const CacheBooks k, const CachePool pool, const int32_t* ws, int slices) {
+    griddep_wait();  // the plan
     const int live = ws[kCompactLive], moves = ws[kCompactMoves];
     const int32_t* list = ws + kCompactList;
     const int32_t* place = list + k.num_blocks;
@@ -753,7 +836,8 @@ inline void launch_compact(const CacheBooks& k, const CachePool& pool, int32_t* 
     const int slices = page_slices(pool.page_bytes);
     mla_cache_compact_plan_kernel<<<1, kBookThreads, 0, stream>>>(k, ws);
     const int64_t most = max((int64_t)k.batch, (int64_t)(k.num_blocks / 2) * slices);
-    mla_cache_compact_kernel<<<(unsigned)min((int64_t)148 * 16, max(most, (int64_t)1)), kMoveThreads, 0, stream>>>(k, pool, ws, slices);
+    launch_after(mla_cache_compact_kernel, dim3((unsigned)min((int64_t)148 * 16, max(most, (int64_t)1))), stream, k, pool,
+                 (const int32_t*)ws, slices);
 }
 
 }  // namespace mla
