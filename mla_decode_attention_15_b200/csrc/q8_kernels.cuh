@@ -83,8 +83,13 @@ struct Q8Cfg {
     static_assert(!kSplitRegs || kRegsIssue + kRegsQ + 2 * kRegsSoftmax <= 4 * 128, "register split");
     static constexpr int kQN = 2 * NG;                      // S^T columns: hi, lo
     static constexpr int kNP = kQ8Terms * NG;               // O^T columns per d_v chunk
-    static constexpr int kSlots = NG == 16 ? 5 : 4;         // ring of 32 KB slots
-    static constexpr int kRopeSlots = NG == 16 ? 3 : 2;     // one per step that the ring can hold, in part or whole
+    // The ring holds two and a half steps.  A step's slots stay taken from its loads
+    // through GEMM1, the softmax and GEMM2, so with two steps the loads of one
+    // wait for the GEMM2 of the other; 32-column groups, whose Q takes 36 KB, make
+    // room for the half by one buffer of P^T instead of two.
+    static constexpr int kSlots = 5;                        // ring of 32 KB slots
+    static constexpr int kRopeSlots = NG == 16 ? 3 : 2;     // RoPE columns of a step
+    static constexpr int kPBufs = NG == 16 ? 2 : 1;
     // shared memory
     static constexpr int kBoxOff = 0;
     static constexpr int kRopeOff = kBoxOff + kSlots * kQ8SlotBytes;
@@ -92,7 +97,7 @@ struct Q8Cfg {
     static constexpr int kQBytes = kQN * kDqk;
     static constexpr int kPOff = kQOff + kQBytes;
     static constexpr int kPBytes = kQ8Step * kNP;
-    static constexpr int kRedOff = kPOff + 2 * kPBytes;     // float [NG][4]
+    static constexpr int kRedOff = kPOff + kPBufs * kPBytes;     // float [NG][4]
     static constexpr int kSumOff = kRedOff + NG * 16;       // float [NG][4]
     static constexpr int kQsOff = kSumOff + NG * 16;        // float [2][NG]: row scale x softmax scale x log2 e, by item
     static constexpr int kVoteOff = kQsOff + 2 * NG * 4;    // uint32 [2][8]
@@ -426,8 +431,8 @@ __device__ void q8_gemm2(const Q8Params& p, const int32_t* meta, uint8_t* smem, 
     bool ok = true;
     while (ok && it.next(p, item)) {
         for (int j = item.p0; j < item.p1; j += 2) {
-            const int pb = s_it & 1;
-            ok = wait_warp(bar0 + 8 * (kQbPFull0 + pb), (s_it >> 1) & 1, ctl);
+            const uint32_t pb = s_it % C::kPBufs;
+            ok = wait_warp(bar0 + 8 * (kQbPFull0 + pb), (s_it / C::kPBufs) & 1, ctl);
             if (!ok) break;
             if (j == item.p0) {
                 ok = wait_warp(bar0 + 8 * kQbOEmpty, (item_it & 1) ^ 1, ctl);
@@ -622,7 +627,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                 R = Rn;
                 if (j > item.p0) {
                     const uint32_t prev = s_it - 1;
-                    ok = wait_warp(bar0 + 8 * (kQbPEmpty0 + (prev & 1)), (prev >> 1) & 1, ctl);
+                    ok = wait_warp(bar0 + 8 * (kQbPEmpty0 + prev % C::kPBufs), (prev / C::kPBufs) & 1, ctl);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
@@ -665,8 +670,8 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                     z[c] *= f;
                 }
             }
-            const int pb = s_it & 1;
-            ok = wait_warp(bar0 + 8 * (kQbPEmpty0 + pb), ((s_it >> 1) & 1) ^ 1, ctl);
+            const uint32_t pb = s_it % C::kPBufs;
+            ok = wait_warp(bar0 + 8 * (kQbPEmpty0 + pb), ((s_it / C::kPBufs) & 1) ^ 1, ctl);
             if (!ok) break;
             q8_store_p(z, pbase + pb * C::kPBytes, kTermStride);
             if (j + 2 >= item.p1 && t >= (end < item.L ? end : item.L)) {
@@ -723,7 +728,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                 p.lpart[(size_t)item.slot * NG + cg * 16 + row] = isnan(lse) ? INFINITY : lse;
             }
         }
-        ok = wait_warp(bar0 + 8 * (kQbPEmpty0 + (last & 1)), (last >> 1) & 1, ctl);
+        ok = wait_warp(bar0 + 8 * (kQbPEmpty0 + last % C::kPBufs), (last / C::kPBufs) & 1, ctl);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
