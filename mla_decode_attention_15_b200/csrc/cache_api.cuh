@@ -74,13 +74,11 @@ int launch_q8(const Plan& pl, const Q8Params& p, const CUtensorMap& kvm, const C
                 cudaGetLastError();
                 return MLA_ERR_CUDA;
             }
-            if constexpr (C::kSplitRegs) {
-                // setmaxnreg.inc waits until the registers it asks for are free in
-                // the CTA: the split must fit the launch as compiled
-                cudaFuncAttributes fa;
-                if (cudaFuncGetAttributes(&fa, mla_decode_q8_kernel<NG>) != cudaSuccess) return MLA_ERR_CUDA;
-                if (fa.numRegs * 4 < C::kRegsIssue + C::kRegsQ + 2 * C::kRegsSoftmax) return MLA_ERR_UNSUPPORTED;
-            }
+            // setmaxnreg.inc waits until the registers it asks for are free in
+            // the CTA: the split must fit the launch as compiled
+            cudaFuncAttributes fa;
+            if (cudaFuncGetAttributes(&fa, mla_decode_q8_kernel<NG>) != cudaSuccess) return MLA_ERR_CUDA;
+            if (C::kSplitRegs && fa.numRegs * 4 < C::kRegsIssue + C::kRegsQ + 2 * C::kRegsSoftmax) return MLA_ERR_UNSUPPORTED;
             done[dev] = true;
         }
     }

@@ -72,15 +72,21 @@ struct Q8Params : FwdParams {
 
 template <int NG>
 struct Q8Cfg {
-    static constexpr int kColGroups = NG / 16;              // softmax groups of 4 warps x 16 columns
+    // Query columns of a softmax thread.  Eight warps serve either group: fewer
+    // columns per thread shorten a step's serial part (16 columns, 8 instead of 16 per
+    // thread: b1 x 1K 19.2 -> 15.8 us, b16 x 64K 131 -> 126 us), but a third and fourth
+    // warp per scheduler only contend (32 columns, 8 per thread: 565 -> 825 us).
+    static constexpr int kCols = NG / 2;
+    static constexpr int kColGroups = 2;                    // softmax groups of 4 warps
     static constexpr int kFirstQ = 4;                       // warps 4..7 split Q
     static constexpr int kFirstSoftmax = 8;
     static constexpr int kThreads = 32 * (kFirstSoftmax + 4 * kColGroups);
-    // 512 threads leave 128 registers each at launch: the issuing and the Q warps give
-    // some of theirs to the softmax (warpgroups: issue, Q, softmax twice).
-    static constexpr bool kSplitRegs = kThreads == 512;
+    // 512 threads leave 128 registers each at launch.  With 16 columns the softmax
+    // needs more: the issuing and the Q warps give some of theirs (warpgroups: issue, Q,
+    // softmax twice).
+    static constexpr bool kSplitRegs = kCols == 16;
     static constexpr int kRegsIssue = 64, kRegsQ = 96, kRegsSoftmax = 176;
-    static_assert(!kSplitRegs || kRegsIssue + kRegsQ + 2 * kRegsSoftmax <= 4 * 128, "register split");
+    static_assert(kThreads == 512 && kRegsIssue + kRegsQ + 2 * kRegsSoftmax <= 4 * 128, "register split");
     static constexpr int kQN = 2 * NG;                      // S^T columns: hi, lo
     static constexpr int kNP = kQ8Terms * NG;               // O^T columns per d_v chunk
     // The ring holds two and a half steps.  A step's slots stay taken from its loads
@@ -163,23 +169,40 @@ __device__ __forceinline__ uint32_t e4m3x2_h2(uint32_t h2) {
     return r;
 }
 
-// Reduces 16 values over the 32 lanes of a warp; lane l returns value l / 2.
-template <bool kMax>
-__device__ __forceinline__ float reduce16(float (&v)[16], int lane) {
+// W (8 or 16) values reduced over the 32 lanes of a warp; lane l returns value l W / 32.
+template <bool kMax, int W>
+__device__ __forceinline__ float reduce_cols(const float (&x)[W], int lane) {
+    float v[W];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-        const int off = 16 >> s, h = 8 >> s;
+    for (int i = 0; i < W; ++i) v[i] = x[i];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const int h = W * off / 32;  // values left after this step; below one, a plain reduction
         const bool upper = (lane & off) != 0;
+        if (h >= 1) {
 #pragma unroll
-        for (int i = 0; i < h; ++i) {
-            const float send = upper ? v[i] : v[i + h];
-            const float keep = upper ? v[i + h] : v[i];
-            const float got = __shfl_xor_sync(kFullMask, send, off);
-            v[i] = kMax ? fmaxf(keep, got) : keep + got;
+            for (int i = 0; i < h; ++i) {
+                const float send = upper ? v[i] : v[i + h];
+                const float keep = upper ? v[i + h] : v[i];
+                const float got = __shfl_xor_sync(kFullMask, send, off);
+                v[i] = kMax ? fmaxf(keep, got) : keep + got;
+            }
+        } else {
+            const float got = __shfl_xor_sync(kFullMask, v[0], off);
+            v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
         }
     }
-    const float got = __shfl_xor_sync(kFullMask, v[0], 1);
-    return kMax ? fmaxf(v[0], got) : v[0] + got;
+    return v[0];
+}
+template <int W>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[W]) {
+    if constexpr (W == 8) tmem_ld_x8(taddr, v);
+    else tmem_ld_x16(taddr, v);
+}
+template <int W>
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const float (&v)[W]) {
+    if constexpr (W == 8) tmem_st_x8(taddr, v);
+    else tmem_st_x16(taddr, v);
 }
 
 // ------------------------------------------------------------------ producer
@@ -473,12 +496,12 @@ __device__ __forceinline__ void q8_drain(uint32_t bar) {
 }
 
 // ------------------------------------------------------------------ softmax
-// 16 weights x (fp16 range) as three e4m3 terms, stored as 16-byte pieces 2 KB
-// times the column groups apart.
-__device__ __forceinline__ void q8_store_p(const float (&x)[16], uint8_t* dst, int term_stride) {
-    uint32_t w[kQ8Terms][4];
+// W weights x (fp16 range) as three e4m3 terms, each term's W bytes term_stride apart.
+template <int W>
+__device__ __forceinline__ void q8_store_p(const float (&x)[W], uint8_t* dst, int term_stride) {
+    uint32_t w[kQ8Terms][W / 4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < W / 2; ++i) {
         __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
 #pragma unroll
         for (int t = 0; t < kQ8Terms; ++t) {
@@ -490,25 +513,28 @@ __device__ __forceinline__ void q8_store_p(const float (&x)[16], uint8_t* dst, i
         }
     }
 #pragma unroll
-    for (int t = 0; t < kQ8Terms; ++t)
-        *reinterpret_cast<uint4*>(dst + t * term_stride) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+    for (int t = 0; t < kQ8Terms; ++t) {
+        if constexpr (W == 8) *reinterpret_cast<uint2*>(dst + t * term_stride) = make_uint2(w[t][0], w[t][1]);
+        else *reinterpret_cast<uint4*>(dst + t * term_stride) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+    }
 }
 
 template <int NG>
 __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem, uint32_t tmem, const Ctl& ctl) {
     using C = Q8Cfg<NG>;
+    constexpr int W = C::kCols;
     const int lane = threadIdx.x & 31;
     const int wq = (threadIdx.x >> 5) & 3;                       // TMEM lane quadrant
-    const int cg = ((threadIdx.x >> 5) - C::kFirstSoftmax) >> 2;  // columns [16 cg, 16 cg + 16)
+    const int cg = ((threadIdx.x >> 5) - C::kFirstSoftmax) >> 2;  // columns [W cg, W cg + W)
     const int row = 32 * wq + lane;                              // token of the step
     const uint32_t tm = tmem + (static_cast<uint32_t>(32 * wq) << 16);
     const uint32_t bar0 = smem_addr(smem + C::kBarOff);
-    float* red = reinterpret_cast<float*>(smem + C::kRedOff) + cg * 64;   // [16][4]: a step's maxima
-    float* sums = reinterpret_cast<float*>(smem + C::kSumOff) + cg * 64;  // [16][4]
-    const float* qs_ring = reinterpret_cast<const float*>(smem + C::kQsOff) + cg * 16;
+    float* red = reinterpret_cast<float*>(smem + C::kRedOff) + cg * W * 4;   // [W][4]: a step's maxima
+    float* sums = reinterpret_cast<float*>(smem + C::kSumOff) + cg * W * 4;  // [W][4]
+    const float* qs_ring = reinterpret_cast<const float*>(smem + C::kQsOff) + cg * W;
     uint32_t* vote = reinterpret_cast<uint32_t*>(smem + C::kVoteOff) + cg * 4;
     constexpr int kTermStride = NG * kQ8Step;
-    uint8_t* pbase = smem + C::kPOff + cg * 16 * kQ8Step + row * 16;
+    uint8_t* pbase = smem + C::kPOff + (cg * W / 16) * 16 * kQ8Step + row * 16 + cg * W % 16;
     const bool causal2 = p.causal && p.s_q > 1;
     auto arrive = [&](uint32_t bar) {  // once per warp, after all of its lanes
         __syncwarp();
@@ -524,7 +550,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
         if (!ok) break;
         arrive(bar0 + 8 * kQbQSeen);
         const float4* qs4 = reinterpret_cast<const float4*>(qs_ring + (item_it & 1) * NG);
-        const int gc0 = item.g * NG + cg * 16;  // first query column of the group
+        const int gc0 = item.g * NG + cg * W;  // first query column of the group
         // Table entries are fetched two steps ahead and page scales one, so
         // that no step waits for either.
         const int32_t* bt = p.block_table + (size_t)item.b * p.max_blocks;
@@ -535,9 +561,9 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
         };
         float sc0 = page_scale(entry(item.p0)), sc1 = page_scale(entry(item.p0 + 1));
         int ph0 = entry(item.p0 + 2), ph1 = entry(item.p0 + 3);
-        float m[16], l[16];
+        float m[W], l[W];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
+        for (int c = 0; c < W; ++c) {
             m[c] = kQ8Unset;
             l[c] = 0.f;
         }
@@ -552,17 +578,17 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             ok = wait_warp(bar0 + 8 * (kQbSFull0 + sb), (s_it >> 1) & 1, ctl);
             if (!ok) break;
             tc_fence_after();
-            float z[16];
+            float z[W];
             {
-                float lo[16];
-                const uint32_t s = tm + C::kSCol + sb * C::kQN + cg * 16;
-                tmem_ld_x16(s, z);
-                tmem_ld_x16(s + NG, lo);
+                float lo[W];
+                const uint32_t s = tm + C::kSCol + sb * C::kQN + cg * W;
+                tmem_ld_cols(s, z);
+                tmem_ld_cols(s + NG, lo);
                 tmem_ld_wait();
                 tc_fence_before();
                 arrive(bar0 + 8 * (kQbSEmpty0 + sb));
 #pragma unroll
-                for (int c4 = 0; c4 < 4; ++c4) {
+                for (int c4 = 0; c4 < W / 4; ++c4) {
                     const float4 f = qs4[c4];
                     z[4 * c4 + 0] = fmaf(lo[4 * c4 + 0], 0.0625f, z[4 * c4 + 0]) * (f.x * ks);
                     z[4 * c4 + 1] = fmaf(lo[4 * c4 + 1], 0.0625f, z[4 * c4 + 1]) * (f.y * ks);
@@ -577,7 +603,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                 // The step holds tokens that some column does not see (past the
                 // length, the causal rule, or no second page).
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
+                for (int c = 0; c < W; ++c) {
                     const int lim = causal2 && gc0 + c < p.heads ? lim0 : item.L;
                     if (t >= lim || t >= end) z[c] = -INFINITY;
                 }
@@ -585,7 +611,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             // Does any weight exceed the running reference by more than 2^kQ8Grow?
             bool grow = false;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) grow |= z[c] > m[c] + kQ8Grow;
+            for (int c = 0; c < W; ++c) grow |= z[c] > m[c] + kQ8Grow;
             const uint32_t gw = __any_sync(kFullMask, grow) ? 1u : 0u;
             if (lane == 0) vote[(s_it & 1) * 8 + wq] = gw;
             const uint32_t vbar = bar0 + 8 * (kQbVote0 + (s_it & 1) * 2 + cg);
@@ -597,21 +623,18 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             const bool grown = (v4.x | v4.y | v4.z | v4.w) != 0;  // the same for the group's four warps
             if (grown || Rn > R) {
                 // Move the references and rescale what is accumulated.
-                float alpha[16];
+                float alpha[W];
                 const float ra = R / Rn;
                 if (grown) {
-                    float zr[16];
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) zr[c] = z[c];
-                    const float wmax = reduce16<true>(zr, lane);
-                    if ((lane & 1) == 0) red[(lane >> 1) * 4 + wq] = wmax;
+                    const float wmax = reduce_cols<true>(z, lane);
+                    if (lane % (32 / W) == 0) red[lane / (32 / W) * 4 + wq] = wmax;
                     arrive(bar0 + 8 * (kQbMax0 + cg));
                     ok = wait_warp(bar0 + 8 * (kQbMax0 + cg), max_it & 1, ctl);
                     ++max_it;
                     if (!ok) break;
                 }
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
+                for (int c = 0; c < W; ++c) {
                     float a = 1.f;
                     if (grown) {
                         const float4 r4 = *reinterpret_cast<const float4*>(red + c * 4);
@@ -630,18 +653,19 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                     ok = wait_warp(bar0 + 8 * (kQbPEmpty0 + prev % C::kPBufs), (prev / C::kPBufs) & 1, ctl);
                     if (!ok) break;
                     tc_fence_after();
+                    constexpr int U = 48 / W;  // accumulators at a time
 #pragma unroll 1
-                    for (int i = 0; i < kQ8Boxes * kQ8Terms; i += 3) {
-                        float o[3][16];
-                        const uint32_t ta = tm + C::kOCol + i * NG + cg * 16;
+                    for (int i = 0; i < kQ8Boxes * kQ8Terms; i += U) {
+                        float o[U][W];
+                        const uint32_t ta = tm + C::kOCol + i * NG + cg * W;
 #pragma unroll
-                        for (int u = 0; u < 3; ++u) tmem_ld_x16(ta + u * NG, o[u]);
+                        for (int u = 0; u < U; ++u) tmem_ld_cols(ta + u * NG, o[u]);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int u = 0; u < 3; ++u) {
+                        for (int u = 0; u < U; ++u) {
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) o[u][c] *= alpha[c];
-                            tmem_st_x16(ta + u * NG, o[u]);
+                            for (int c = 0; c < W; ++c) o[u][c] *= alpha[c];
+                            tmem_st_cols(ta + u * NG, o[u]);
                         }
                     }
                     tmem_st_wait();
@@ -655,7 +679,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             }
             if (bias > kQ8MinBias) {
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
+                for (int c = 0; c < W; ++c) {
                     z[c] = ex2_approx(z[c] - m[c] + bias);
                     l[c] = fmaf(z[c], back, l[c]);
                 }
@@ -664,7 +688,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                 // page's still counts in full in the sum of the weights.
                 const float f = exp2f(bias);
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
+                for (int c = 0; c < W; ++c) {
                     z[c] = ex2_approx(z[c] - m[c]);
                     l[c] += z[c];
                     z[c] *= f;
@@ -700,23 +724,23 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
 
         // ---- epilogue ----
         {
-            const float wsum = reduce16<false>(l, lane);
-            if ((lane & 1) == 0) sums[(lane >> 1) * 4 + wq] = wsum;
+            const float wsum = reduce_cols<false>(l, lane);
+            if (lane % (32 / W) == 0) sums[lane / (32 / W) * 4 + wq] = wsum;
         }
         arrive(bar0 + 8 * (kQbSum0 + cg));
         ok = wait_warp(bar0 + 8 * (kQbSum0 + cg), item_it & 1, ctl);
         if (!ok) break;
         const uint32_t last = s_it - 1;
-        float inv[16], m_own = 0.f, l_own = 0.f;
+        float inv[W], m_own = 0.f, l_own = 0.f;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
+        for (int c = 0; c < W; ++c) {
             const float4 s4 = *reinterpret_cast<const float4*>(sums + c * 4);
             const float ls = (s4.x + s4.y) + (s4.z + s4.w);
             inv[c] = ls == 0.f ? 0.f : __fdividef(R * 0.0625f, ls);
             m_own = row == c ? m[c] : m_own;
             l_own = row == c ? ls : l_own;
         }
-        if (row < 16 && gc0 + row < p.N) {
+        if (row < W && gc0 + row < p.N) {
             const int gc = gc0 + row;
             const float lse = l_own == 0.f ? -INFINITY : (m_own + log2f(l_own)) * kLn2;
             if (item.unsplit) {
@@ -725,7 +749,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             } else if (item.slot >= 0) {
                 // (the combine's maximum passes over a NaN; an infinity makes its
                 // weights NaN, and so the merged row)
-                p.lpart[(size_t)item.slot * NG + cg * 16 + row] = isnan(lse) ? INFINITY : lse;
+                p.lpart[(size_t)item.slot * NG + cg * W + row] = isnan(lse) ? INFINITY : lse;
             }
         }
         ok = wait_warp(bar0 + 8 * (kQbPEmpty0 + last % C::kPBufs), (last / C::kPBufs) & 1, ctl);
@@ -733,18 +757,18 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
         tc_fence_after();
 #pragma unroll 1
         for (int ch = 0; ch < kQ8Boxes; ++ch) {
-            float o[16], o1[16], o2[16];
-            const uint32_t ta = tm + C::kOCol + ch * C::kNP + cg * 16;
-            tmem_ld_x16(ta, o);
-            tmem_ld_x16(ta + NG, o1);
-            tmem_ld_x16(ta + 2 * NG, o2);
+            float o[W], o1[W], o2[W];
+            const uint32_t ta = tm + C::kOCol + ch * C::kNP + cg * W;
+            tmem_ld_cols(ta, o);
+            tmem_ld_cols(ta + NG, o1);
+            tmem_ld_cols(ta + 2 * NG, o2);
             tmem_ld_wait();
             const int d = ch * 128 + row;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
+            for (int c = 0; c < W; ++c) {
                 const float v = fmaf(fmaf(o2[c], 0.0625f, o1[c]), 0.0625f, o[c]) * inv[c];
                 if (!item.unsplit) {
-                    if (item.slot >= 0) p.opart[((size_t)item.slot * NG + cg * 16 + c) * kDv + d] = v;
+                    if (item.slot >= 0) p.opart[((size_t)item.slot * NG + cg * W + c) * kDv + d] = v;
                 } else if (gc0 + c < p.N) {
                     const size_t at = ((size_t)item.b * p.N + gc0 + c) * kDv + d;
                     if (p.out_f32) static_cast<float*>(p.out)[at] = v;
