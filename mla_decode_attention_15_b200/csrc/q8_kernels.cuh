@@ -112,10 +112,13 @@ struct Q8Cfg {
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kPlanMetaOff = kMiscOff + 16;
     static constexpr int kBytes = kPlanMetaOff + (kMetaWords + 8) * 4;
+    // Plans of up to kSmallPlan work items keep their prefix where P^T goes, and one
+    // idle warp publishes them while the others begin; the first P^T waits for it.
+    static constexpr int kSmallPlan = kPBufs * kPBytes / 4 - 48;
     static constexpr int kAlloc = kBytes + 1024;
     static_assert(kAlloc <= 227 * 1024, "shared memory budget");
     static_assert(kQOff % 1024 == 0 && kPOff % 128 == 0 && kPBytes % 128 == 0, "operand alignment");
-    // the plan's scratch: slots past the first step's boxes
+    // larger plans: the slots past the first step's
     static constexpr int kInlinePlanMaxBG = (kSlots - kQ8Halves) * kQ8SlotBytes / 4 - 48;
     // TMEM columns
     static constexpr int kSCol = 0;
@@ -128,7 +131,7 @@ struct Q8Cfg {
 constexpr int kQ8MaxSlots = 5;
 enum Q8Bar {
     kQbQFull = 0, kQbQEmpty, kQbSFull0, kQbSFull1, kQbSEmpty0, kQbSEmpty1, kQbPFull0, kQbPFull1, kQbPEmpty0, kQbPEmpty1,
-    kQbOEmpty, kQbDone1, kQbDone2, kQbQSeen,
+    kQbOEmpty, kQbDone1, kQbDone2, kQbQSeen, kQbPlan,
     kQbVote0,                            // [2 parities][2 column groups]
     kQbMax0 = kQbVote0 + 4,              // [2 column groups]
     kQbSum0 = kQbMax0 + 2,               // [2 column groups]
@@ -281,92 +284,102 @@ __device__ void q8_producer(const CUtensorMap* kv_map, const CUtensorMap* rope_m
 }
 
 // ------------------------------------------------------------------ Q split
-// Four warps cut the item's query rows into hi and lo terms while the previous
-// item's softmax and epilogue run: 8 lanes per row, 16 rows at a time.  The
-// result is GEMM1's K-major B operand without swizzle: 16-byte pieces, piece
-// (k, n) of K bytes [16 k, 16 k + 16) and column n at (k * kQN + n) * 16.
+// Cuts a query row into hi and lo terms, 8 lanes per row.  The result is GEMM1's
+// K-major B operand without swizzle: 16-byte pieces, piece (k, n) of K bytes
+// [16 k, 16 k + 16) and column n at (k * kQN + n) * 16; `dst` is piece (0, n) of the
+// row's hi term, `row` null for a column past the last.  Every CTA runs this once before
+// anything else can start, with a cold instruction cache, so it is a loop of a few
+// instructions: unrolled over the row it took 4,200
+// cycles (32 columns: 7,900).
+template <int NG>
+__device__ __forceinline__ void q8_split_row(const __nv_bfloat16* row, uint8_t* dst, float* scale_out, float scale_log2) {
+    using C = Q8Cfg<NG>;
+    const int lane8 = threadIdx.x & 7;
+    uint4 raw[9];
+#pragma unroll
+    for (int i = 0; i < 9; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+    if (row != nullptr) {
+        // (plain loads: a read-only load may be scheduled above the wait on the grid that wrote q)
+#pragma unroll
+        for (int i = 0; i < 9; ++i) raw[i] = reinterpret_cast<const uint4*>(row)[i * 8 + lane8];
+    }
+    uint32_t top = 0;  // two bf16 magnitudes as bits: non-finite values are the largest
+#pragma unroll
+    for (int i = 0; i < 9; ++i)
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
+                                     __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu)));
+    uint32_t amax = max(top << 16, top & 0x7fff0000u);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(kFullMask, amax, o));
+    const int ex = amax == 0 ? 0 : max(e4m3_scale_exp(amax), -100);
+    // a row with an infinity or a NaN becomes NaN: so do its scores
+    const float inv = amax >= kInfBits ? __int_as_float(0x7fffffff) : pow2f(-ex);
+    if (lane8 == 0) *scale_out = (amax >= kInfBits ? 1.f : pow2f(ex)) * scale_log2;
+    uint8_t* d = dst + (lane8 >> 1) * (C::kQN * 16) + (lane8 & 1) * 8;
+#pragma unroll 1
+    for (int i = 0; i < 9; ++i) {
+        const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            // scaled to at most 448, fp16 holds the 8 bits down to 2^-17, and its
+            // last place (2^-24) is far below the last place of lo
+            const __half2 x = __floats2half2_rn(__uint_as_float(w[e] << 16) * inv, __uint_as_float(w[e] & 0xffff0000u) * inv);
+            const uint32_t h = e4m3x2_h2(as_u32(x));
+            const uint32_t l = e4m3x2_h2(as_u32(__hmul2(__hsub2(x, as_h2(h2_of_e4m3x2(h))), __float2half2_rn(16.f))));
+            if (e & 1) {
+                hi[e >> 1] |= h << 16;
+                lo[e >> 1] |= l << 16;
+            } else {
+                hi[e >> 1] = h;
+                lo[e >> 1] = l;
+            }
+        }
+        *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(d + NG * 16) = make_uint2(lo[0], lo[1]);
+        d += 4 * C::kQN * 16;  // 64 columns on
+#pragma unroll
+        for (int k = 0; k < 8; ++k) raw[k] = raw[k + 1];
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+template <int NG>
+__device__ __forceinline__ void q8_split(const Q8Params& p, const Item& item, uint8_t* smem, int col, uint32_t q_it) {
+    using C = Q8Cfg<NG>;
+    const int gc = item.g * NG + col;
+    q8_split_row<NG>(gc < p.N ? p.q + ((size_t)item.b * p.N + gc) * kDqk : nullptr, smem + C::kQOff + col * 16,
+                     reinterpret_cast<float*>(smem + C::kQsOff) + (q_it & 1) * NG + col, p.scale_log2);
+}
+
+// Four warps split each item's Q, 16 rows at a time, while the previous item's
+// softmax and epilogue run.  Of the first item, which the whole CTA waits for, softmax
+// warps take the rows past the first 16.
 template <int NG>
 __device__ void q8_split_q(const Q8Params& p, const int32_t* meta, uint8_t* smem, const Ctl& ctl) {
     using C = Q8Cfg<NG>;
     const uint32_t bar0 = smem_addr(smem + C::kBarOff);
     const int tid = threadIdx.x - 32 * C::kFirstQ;
-    const int lane8 = tid & 7;
-    float* qs = reinterpret_cast<float*>(smem + C::kQsOff);
     WorkIter it;
     it.init(meta, p);
     Item item;
     uint32_t q_it = 0;
     while (it.next(p, item)) {
-        bool ready = false;
-#pragma unroll 1
-        for (int pass = 0; pass < NG / 16; ++pass) {
-            const int col = pass * 16 + (tid >> 3);
-            const int gc = item.g * NG + col;
-            uint4 raw[9];
-#pragma unroll
-            for (int i = 0; i < 9; ++i) raw[i] = make_uint4(0, 0, 0, 0);
-            if (gc < p.N) {
-                // (plain loads: a read-only load may be scheduled above the wait on the grid that wrote q)
-                const uint4* row = reinterpret_cast<const uint4*>(p.q + ((size_t)item.b * p.N + gc) * kDqk);
-#pragma unroll
-                for (int i = 0; i < 9; ++i) raw[i] = row[i * 8 + lane8];
-            }
-            uint32_t amax = 0;  // as bits of |x|: non-finite values are the largest
-#pragma unroll
-            for (int i = 0; i < 9; ++i) {
-                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    amax = max(amax, (w[e] << 16) & 0x7fffffffu);
-                    amax = max(amax, w[e] & 0x7fff0000u);
-                }
-            }
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(kFullMask, amax, o));
-            int ex = e4m3_scale_exp(amax);
-            ex = amax == 0 ? 0 : max(ex, -100);
-            // a row with an infinity or a NaN becomes NaN: so do its scores
-            const float inv = amax >= 0x7f800000u ? __int_as_float(0x7fffffff) : pow2f(-ex);
-            if (!ready) {
-                // GEMM1 of the previous item has read its Q, and its softmax has
-                // begun (so it is past its wait on kQbQFull, and done with the
-                // row scales of the item before).
-                for (int i = 0; i < kQ8MaxNaps && !mbar_try_wait(bar0 + 8 * kQbQEmpty, (q_it & 1) ^ 1) && !*ctl.abort_flag; ++i)
-                    __nanosleep(kQ8Nap);
-                if (!wait_warp(bar0 + 8 * kQbQEmpty, (q_it & 1) ^ 1, ctl)) return;
-                if (!wait_warp(bar0 + 8 * kQbQSeen, (q_it & 1) ^ 1, ctl)) return;
-                ready = true;
-            }
-            if (lane8 == 0)
-                qs[(q_it & 1) * NG + col] = (amax >= 0x7f800000u ? 1.f : pow2f(ex)) * p.scale_log2;
-            uint8_t* dst = smem + C::kQOff + col * 16;
-#pragma unroll
-            for (int i = 0; i < 9; ++i) {
-                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-                uint32_t hi[2], lo[2];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float a = __uint_as_float(w[e] << 16) * inv, b = __uint_as_float(w[e] & 0xffff0000u) * inv;
-                    const uint32_t h = e4m3x2(a, b);
-                    const float2 back = __half22float2(as_h2(h2_of_e4m3x2(h)));
-                    const uint32_t l = e4m3x2((a - back.x) * 16.f, (b - back.y) * 16.f);
-                    if (e & 1) {
-                        hi[e >> 1] |= h << 16;
-                        lo[e >> 1] |= l << 16;
-                    } else {
-                        hi[e >> 1] = h;
-                        lo[e >> 1] = l;
-                    }
-                }
-                const int kb = (i * 8 + lane8) * 8;
-                uint8_t* d = dst + (kb >> 4) * (C::kQN * 16) + (kb & 15);
-                *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2*>(d + NG * 16) = make_uint2(lo[0], lo[1]);
-            }
+        if (q_it > 0) {
+            // GEMM1 of the previous item has read its Q, and its softmax has begun
+            // (so it is past its wait on kQbQFull, and done with the row scales of
+            // the item before).
+            for (int i = 0; i < kQ8MaxNaps && !mbar_try_wait(bar0 + 8 * kQbQEmpty, (q_it & 1) ^ 1) && !*ctl.abort_flag; ++i)
+                __nanosleep(kQ8Nap);
+            if (!wait_warp(bar0 + 8 * kQbQEmpty, (q_it & 1) ^ 1, ctl)) return;
+            if (!wait_warp(bar0 + 8 * kQbQSeen, (q_it & 1) ^ 1, ctl)) return;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if ((tid & 31) == 0) mbar_arrive(bar0 + 8 * kQbQFull);
+        const int rows = q_it == 0 ? 16 : NG;
+#pragma unroll 1
+        for (int r = 0; r < rows; r += 16) {
+            q8_split<NG>(p, item, smem, r + (tid >> 3), q_it);
+            if ((tid & 31) == 0) mbar_arrive(bar0 + 8 * kQbQFull);
+        }
         ++q_it;
     }
 }
@@ -520,7 +533,8 @@ __device__ __forceinline__ void q8_store_p(const float (&x)[W], uint8_t* dst, in
 }
 
 template <int NG>
-__device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem, uint32_t tmem, const Ctl& ctl) {
+__device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem, uint32_t tmem, const Ctl& ctl,
+                           bool plan_in_p) {
     using C = Q8Cfg<NG>;
     constexpr int W = C::kCols;
     const int lane = threadIdx.x & 31;
@@ -546,6 +560,12 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
     uint32_t s_it = 0, item_it = 0, max_it = 0;
     bool ok = true;
     while (ok && it.next(p, item)) {
+        if constexpr (NG > 16) {
+            if (item_it == 0 && cg == 0) {
+                q8_split<NG>(p, item, smem, 16 + (row >> 3), 0);
+                arrive(bar0 + 8 * kQbQFull);
+            }
+        }
         ok = wait_warp(bar0 + 8 * kQbQFull, item_it & 1, ctl);
         if (!ok) break;
         arrive(bar0 + 8 * kQbQSeen);
@@ -609,30 +629,42 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                 }
             }
             // Does any weight exceed the running reference by more than 2^kQ8Grow?
-            bool grow = false;
-#pragma unroll
-            for (int c = 0; c < W; ++c) grow |= z[c] > m[c] + kQ8Grow;
-            const uint32_t gw = __any_sync(kFullMask, grow) ? 1u : 0u;
-            if (lane == 0) vote[(s_it & 1) * 8 + wq] = gw;
+            // The first step, which sets the reference, exchanges its maxima at once.
+            const bool first = j == item.p0;
             const uint32_t vbar = bar0 + 8 * (kQbVote0 + (s_it & 1) * 2 + cg);
+            auto post_maxima = [&]() {
+                const float wmax = reduce_cols<true>(z, lane);
+                if (lane % (32 / W) == 0) red[lane / (32 / W) * 4 + wq] = wmax;
+            };
+            if (first) {
+                post_maxima();
+            } else {
+                bool grow = false;
+#pragma unroll
+                for (int c = 0; c < W; ++c) grow |= z[c] > m[c] + kQ8Grow;
+                const uint32_t gw = __any_sync(kFullMask, grow) ? 1u : 0u;
+                if (lane == 0) vote[(s_it & 1) * 8 + wq] = gw;
+            }
             arrive(vbar);
             ok = wait_warp(vbar, (s_it >> 1) & 1, ctl);
             if (!ok) break;
-            const uint4 v4 = *reinterpret_cast<const uint4*>(vote + (s_it & 1) * 8);
             const float Rn = fmaxf(R, fmaxf(sc0, sc1));
-            const bool grown = (v4.x | v4.y | v4.z | v4.w) != 0;  // the same for the group's four warps
+            bool grown = first;
+            if (!first) {
+                const uint4 v4 = *reinterpret_cast<const uint4*>(vote + (s_it & 1) * 8);
+                grown = (v4.x | v4.y | v4.z | v4.w) != 0;  // the same for the group's four warps
+            }
             if (grown || Rn > R) {
                 // Move the references and rescale what is accumulated.
-                float alpha[W];
-                const float ra = R / Rn;
-                if (grown) {
-                    const float wmax = reduce_cols<true>(z, lane);
-                    if (lane % (32 / W) == 0) red[lane / (32 / W) * 4 + wq] = wmax;
+                if (grown && !first) {
+                    post_maxima();
                     arrive(bar0 + 8 * (kQbMax0 + cg));
                     ok = wait_warp(bar0 + 8 * (kQbMax0 + cg), max_it & 1, ctl);
                     ++max_it;
                     if (!ok) break;
                 }
+                const float ra = R / Rn;
+                float alpha[W];
 #pragma unroll
                 for (int c = 0; c < W; ++c) {
                     float a = 1.f;
@@ -697,6 +729,11 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             const uint32_t pb = s_it % C::kPBufs;
             ok = wait_warp(bar0 + 8 * (kQbPEmpty0 + pb), ((s_it / C::kPBufs) & 1) ^ 1, ctl);
             if (!ok) break;
+            if (plan_in_p) {  // the plan's scratch lies there until it is published
+                ok = wait_warp(bar0 + 8 * kQbPlan, 0, ctl);
+                if (!ok) break;
+                plan_in_p = false;
+            }
             q8_store_p(z, pbase + pb * C::kPBytes, kTermStride);
             if (j + 2 >= item.p1 && t >= (end < item.L ? end : item.L)) {
                 // Rows behind the sequence, or of an absent second page: their
@@ -755,7 +792,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
         ok = wait_warp(bar0 + 8 * (kQbPEmpty0 + last % C::kPBufs), (last / C::kPBufs) & 1, ctl);
         if (!ok) break;
         tc_fence_after();
-#pragma unroll 1
+#pragma unroll (W == 8 ? 2 : 1)
         for (int ch = 0; ch < kQ8Boxes; ++ch) {
             float o[W], o1[W], o2[W];
             const uint32_t ta = tm + C::kOCol + ch * C::kNP + cg * W;
@@ -783,6 +820,50 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
     }
 }
 
+// publish_plan_in_cta for one warp: this CTA's row of the plan, the rows of the work items
+// whose first page it holds, and CTA 0's header and prefix.
+__device__ void q8_publish(const FwdParams& p, int NG, const int32_t* prefix, const int32_t* plan_s) {
+    const int lane = threadIdx.x & 31;
+    const int k = blockIdx.x / p.share, G = gridDim.x / p.share, BG = p.BG;
+    const bool writer = blockIdx.x % p.share == 0;  // group 0 of a shared range writes its rows
+    const int64_t T = plan_s[kPlanT];
+    if (lane < kMetaWords && writer) p.plan_out[kHdrWords + (size_t)k * kMetaWords + lane] = plan_s[lane];
+    int32_t* bginfo = p.plan_out + bg_offset_words(G);
+    int slots = 0;
+    for (int bg = lane; bg < BG; bg += 32) {
+        const int P = pages_in_prefix(prefix, bg);
+        const int ns = num_splits_of(prefix, bg, P, T);
+        if (ns > 1) slots += ns;
+        int owner = P > 0 ? first_cta_of(prefix, bg, T) : 0;
+        if (owner > G - 1) owner = G - 1;
+        if (owner == k && writer) {
+            bginfo[kBgWords * bg] = ns > 1 ? first_split_slot(prefix, bg, T) : 0;
+            bginfo[kBgWords * bg + 1] = ns;
+        }
+    }
+    if (blockIdx.x != 0) return;
+    int32_t* pg = p.plan_out + prefix_offset_words(G, BG);
+    for (int i = lane; i <= BG; i += 32) pg[i] = prefix[i];
+    slots = __reduce_add_sync(kFullMask, slots);
+    if (lane == 0) {
+        int32_t* h = p.plan_out;
+        h[kHdrMagic] = kSchedMagic;
+        h[kHdrG] = G;
+        h[kHdrBG] = BG;
+        h[kHdrHg] = p.Hg;
+        h[kHdrNG] = NG;
+        h[kHdrSlots] = slots;
+        h[kHdrT] = (int)T;
+        h[kHdrW] = plan_s[kPlanW];
+        h[kHdrBatch] = BG / p.Hg;
+        h[kHdrMaxBlocks] = p.max_blocks;
+        h[kHdrShift] = kPageShift;
+        h[kHdrShareHg] = p.share;
+        for (int i = kHdrShareHg + 1; i < kHdrWords; ++i) h[i] = 0;
+        if (plan_s[kPlanBad]) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
+    }
+}
+
 // ------------------------------------------------------------------ kernel
 template <int NG>
 __global__ void __launch_bounds__(Q8Cfg<NG>::kThreads, 1)
@@ -805,7 +886,8 @@ __global__ void __launch_bounds__(Q8Cfg<NG>::kThreads, 1)
             uint32_t count = 1;
             if (i == kQbSEmpty0 || i == kQbSEmpty1 || i == kQbPFull0 || i == kQbPFull1 || i == kQbOEmpty || i == kQbQSeen)
                 count = kSm;
-            if ((i >= kQbVote0 && i < kQbFull0) || i == kQbQFull) count = 4;
+            if (i >= kQbVote0 && i < kQbFull0) count = 4;
+            if (i == kQbQFull) count = NG / 4;  // 4 rows per warp
             mbar_init(bar0 + 8 * i, count);
         }
         *abort_flag = 0;
@@ -822,7 +904,9 @@ __global__ void __launch_bounds__(Q8Cfg<NG>::kThreads, 1)
     tc_fence_after();
     // The plan from the lengths, and the first step's pages, before the wait on
     // the grid before this one (see mla_decode_fwd_kernel).
-    int32_t* plan_scratch = reinterpret_cast<int32_t*>(smem + C::kBoxOff + kQ8Halves * kQ8SlotBytes);
+    const bool small_plan = p.BG <= C::kSmallPlan;
+    int32_t* plan_scratch =
+        reinterpret_cast<int32_t*>(smem + (small_plan ? C::kPOff : C::kBoxOff + kQ8Halves * kQ8SlotBytes));
     bool first_issued = false;
     if (p.plan_out != nullptr) {
         build_plan_in_cta(p, plan_scratch, meta_s);
@@ -847,8 +931,10 @@ __global__ void __launch_bounds__(Q8Cfg<NG>::kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const int32_t* meta;
     if (p.plan_out != nullptr) {
-        fence_proxy_async_smem();  // the scratch, before copies land there
-        publish_plan_in_cta(p, NG, plan_scratch, meta_s);
+        if (!small_plan) {
+            fence_proxy_async_smem();  // the scratch, before copies land there
+            publish_plan_in_cta(p, NG, plan_scratch, meta_s);
+        }
         meta = meta_s;
     } else {
         const int32_t* hdr = p.sched;
@@ -866,7 +952,7 @@ __global__ void __launch_bounds__(Q8Cfg<NG>::kThreads, 1)
     const Ctl ctl{abort_flag, p.status};
     if (warp >= C::kFirstSoftmax) {
         if constexpr (C::kSplitRegs) setmaxnreg_inc<C::kRegsSoftmax>();
-        q8_softmax<NG>(p, meta, smem, tmem, ctl);
+        q8_softmax<NG>(p, meta, smem, tmem, ctl, p.plan_out != nullptr && small_plan);
     } else if (warp >= C::kFirstQ) {
         if constexpr (C::kSplitRegs) setmaxnreg_dec<C::kRegsQ>();
         q8_split_q<NG>(p, meta, smem, ctl);
@@ -880,6 +966,10 @@ __global__ void __launch_bounds__(Q8Cfg<NG>::kThreads, 1)
         } else if (warp == 2) {
             q8_gemm2<NG>(p, meta, smem, tmem, ctl);
             q8_drain(bar0 + 8 * kQbDone2);
+        } else if (p.plan_out != nullptr && small_plan) {
+            q8_publish(p, NG, plan_scratch, meta_s);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar0 + 8 * kQbPlan);
         }
     }
     tc_fence_before();
