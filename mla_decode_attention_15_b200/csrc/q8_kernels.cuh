@@ -792,7 +792,14 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
         ok = wait_warp(bar0 + 8 * (kQbPEmpty0 + last % C::kPBufs), (last / C::kPBufs) & 1, ctl);
         if (!ok) break;
         tc_fence_after();
-#pragma unroll (W == 8 ? 2 : 1)
+        // Output column d of the chunk is this thread's lane: 32 lanes store 32
+        // consecutive values of one query column.
+        const bool f32 = !item.unsplit || p.out_f32;
+        const int cols = item.unsplit ? p.N - gc0 : item.slot >= 0 ? W : 0;
+        const size_t base = (item.unsplit ? (size_t)item.b * p.N + gc0 : (size_t)item.slot * NG + cg * W) * kDv + row;
+        float* dst = (item.unsplit ? static_cast<float*>(p.out) : p.opart) + base;
+        __nv_bfloat16* dst16 = static_cast<__nv_bfloat16*>(p.out) + base;
+#pragma unroll 1
         for (int ch = 0; ch < kQ8Boxes; ++ch) {
             float o[W], o1[W], o2[W];
             const uint32_t ta = tm + C::kOCol + ch * C::kNP + cg * W;
@@ -800,18 +807,19 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             tmem_ld_cols(ta + NG, o1);
             tmem_ld_cols(ta + 2 * NG, o2);
             tmem_ld_wait();
-            const int d = ch * 128 + row;
 #pragma unroll
-            for (int c = 0; c < W; ++c) {
-                const float v = fmaf(fmaf(o2[c], 0.0625f, o1[c]), 0.0625f, o[c]) * inv[c];
-                if (!item.unsplit) {
-                    if (item.slot >= 0) p.opart[((size_t)item.slot * NG + cg * W + c) * kDv + d] = v;
-                } else if (gc0 + c < p.N) {
-                    const size_t at = ((size_t)item.b * p.N + gc0 + c) * kDv + d;
-                    if (p.out_f32) static_cast<float*>(p.out)[at] = v;
-                    else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
-                }
+            for (int c = 0; c < W; ++c) o[c] = fmaf(fmaf(o2[c], 0.0625f, o1[c]), 0.0625f, o[c]) * inv[c];
+            if (f32) {
+#pragma unroll
+                for (int c = 0; c < W; ++c)
+                    if (c < cols) dst[c * kDv] = o[c];
+            } else {
+#pragma unroll
+                for (int c = 0; c < W; ++c)
+                    if (c < cols) dst16[c * kDv] = __float2bfloat16_rn(o[c]);
             }
+            dst += 128;
+            dst16 += 128;
         }
         if (!item.unsplit && item.slot < 0 && row == 0) atomicOr(p.status, MLA_STATUS_BAD_SCHEDULE);
         tc_fence_before();
