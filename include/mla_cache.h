@@ -200,11 +200,11 @@ int mla_cache_compact(const mla_cache_dims* dims, int32_t* block_table, const in
  * The schedule and workspace sizes come from the two _bytes calls below, and
  * the plan from these get_schedule calls (the query groups are 16 or 32
  * columns wide).  MLA_FLAG_INLINE_PLAN builds the plan in the decode kernel up
- * to 28,624 work items (batch x query groups; 20,432 for heads * s_q > 16).
+ * to 24,528 requests (above that the call enqueues the schedule kernel).
  *
  * The cache's bytes are multiplied as they are; neither the query nor the
- * softmax weights are rounded to 8 bits: a query row is within 2^-22 of its
- * largest magnitude, a weight within 2^-12 of itself or 2^-22 of the largest.
+ * softmax weights are rounded to 8 bits: a query value is within 2^-21 of its
+ * row's largest magnitude, a weight within 2^-12 of itself or 2^-22 of the largest.
  * Rows past a request's length, and its last page's unused rows, may hold
  * anything.  A NaN in a row that one query token sees reaches every query token
  * of its request.

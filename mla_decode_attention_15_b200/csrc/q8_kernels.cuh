@@ -16,7 +16,7 @@
 //     power of two per query row (its largest magnitude then lies in (224, 448]),
 //     hi = e4m3(x) leaves a remainder of at most 4 significant bits, which
 //     lo = e4m3(16 (x - hi)) holds exactly.  Only values below 2^-14 of the
-//     row's largest are rounded, by at most 2^-22 of it.  S^T = S_hi + S_lo / 16.
+//     row's largest are rounded, by at most 2^-21 of it.  S^T = S_hi + S_lo / 16.
 //   - P.  x = 16 p s / R (s the page's scale, R the largest scale so far) is rounded
 //     to fp16 (11 bits, half a step is 2^-12 of the weight: an eighth of the
 //     rounding of a bf16 result) and cut into three e4m3 terms, each 16 times the
