@@ -667,15 +667,12 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                 float alpha[W];
 #pragma unroll
                 for (int c = 0; c < W; ++c) {
-                    float a = 1.f;
-                    if (grown) {
-                        const float4 r4 = *reinterpret_cast<const float4*>(red + c * 4);
-                        const float mx = fmaxf(fmaxf(r4.x, r4.y), fmaxf(r4.z, r4.w));
-                        if (mx > m[c] + kQ8Grow) {
-                            a = ex2_approx(m[c] - mx);
-                            m[c] = mx;
-                        }
-                    }
+                    // (without branches: a column that stays has a = 2^0)
+                    const float4 r4 = *reinterpret_cast<const float4*>(red + c * 4);
+                    const float mx = fmaxf(fmaxf(r4.x, r4.y), fmaxf(r4.z, r4.w));
+                    const float to = grown && mx > m[c] + kQ8Grow ? mx : m[c];
+                    const float a = ex2_approx(m[c] - to);
+                    m[c] = to;
                     l[c] *= a;
                     alpha[c] = a * ra;
                 }
@@ -773,7 +770,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
         for (int c = 0; c < W; ++c) {
             const float4 s4 = *reinterpret_cast<const float4*>(sums + c * 4);
             const float ls = (s4.x + s4.y) + (s4.z + s4.w);
-            inv[c] = ls == 0.f ? 0.f : __fdividef(R * 0.0625f, ls);
+            inv[c] = ls == 0.f ? 0.f : R * 0.0625f * rcp_approx(ls);
             m_own = row == c ? m[c] : m_own;
             l_own = row == c ? ls : l_own;
         }
@@ -781,7 +778,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             const int gc = gc0 + row;
             const float lse = l_own == 0.f ? -INFINITY : (m_own + log2f(l_own)) * kLn2;
             if (item.unsplit) {
-                const int sq = gc / p.heads;
+                const int sq = gc >= p.heads ? 1 : 0;  // (at most two query tokens)
                 p.lse[((size_t)item.b * p.heads + (gc - sq * p.heads)) * p.s_q + sq] = lse;
             } else if (item.slot >= 0) {
                 // (the combine's maximum passes over a NaN; an infinity makes its
