@@ -86,7 +86,7 @@ int mla_rope_init(const mla_rope_config* config, mla_rope_table* table);
 
 typedef struct mla_rope_dims {
     int32_t tokens;      /* T >= 0 (0: nothing to do) */
-    int32_t num_heads;   /* h >= 1 */
+    int32_t num_heads;   /* h, 1 .. 65535 */
     int32_t width;       /* values per head row, 64 .. 2048, a multiple of 8 */
     int32_t offset;      /* first of the 64 rotary columns, a multiple of 8, offset + 64 <= width */
     int64_t x_token_stride, x_head_stride;      /* of x, in values: multiples of 8 */

@@ -282,7 +282,7 @@ int mla_rope_init(const mla_rope_config* c, mla_rope_table* t) {
 int mla_rope_apply(const mla_rope_dims* d, const mla_rope_table* table, const void* x, const int32_t* positions, void* out,
                    void* stream) {
     if (d == nullptr || table == nullptr) return MLA_ERR_INVALID_ARG;
-    if (d->tokens < 0 || d->num_heads < 1 || d->width < 2 * kRopePairs || d->width > 2048 || d->width % 8 != 0 ||
+    if (d->tokens < 0 || d->num_heads < 1 || d->num_heads > 65535 || d->width < 2 * kRopePairs || d->width > 2048 || d->width % 8 != 0 ||
         d->offset < 0 || d->offset % 8 != 0 || d->offset + 2 * kRopePairs > d->width ||
         (d->transpose != 0 && d->transpose != 1))
         return MLA_ERR_INVALID_ARG;
@@ -298,7 +298,8 @@ int mla_rope_apply(const mla_rope_dims* d, const mla_rope_table* table, const vo
     if (x == out && (st[0] != st[2] || st[1] != st[3])) return MLA_ERR_INVALID_ARG;
     if (d->tokens == 0) return MLA_OK;
     if (!aligned16(x) || !aligned16(out) || !aligned4(positions)) return MLA_ERR_INVALID_ARG;
-    return launch_rope(*d, *table, x, positions, out, static_cast<cudaStream_t>(stream)) ? launched() : MLA_ERR_UNSUPPORTED;
+    launch_rope(*d, *table, x, positions, out, static_cast<cudaStream_t>(stream));
+    return launched();
 }
 
 int mla_cache_append(const mla_cache_dims* d, int32_t tokens, const void* c_kv, int64_t c_stride, const void* k_pe,

@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kMoveThreads, sizeof(E) == 2 ? 6 : 4) mla_rope
     }
 }
 
-inline bool launch_rope(const mla_rope_dims& d, const mla_rope_table& table, const void* x, const int32_t* positions, void* out,
+inline void launch_rope(const mla_rope_dims& d, const mla_rope_table& table, const void* x, const int32_t* positions, void* out,
                         cudaStream_t stream) {
     RopeParams p = {};
     p.x = x;
@@ -230,7 +230,6 @@ inline bool launch_rope(const mla_rope_dims& d, const mla_rope_table& table, con
     p.hpc = min(d.num_heads, want);
     p.tpc = min(min(kRopeMaxTokens, d.tokens), max(1, want / p.hpc));
     const dim3 grid((d.tokens + p.tpc - 1) / p.tpc, (d.num_heads + p.hpc - 1) / p.hpc);
-    if (grid.y > 65535) return false;
     const int threads = (p.rows_pass * p.per_row + 31) / 32 * 32;
     if (d.dtype == MLA_DTYPE_BF16) {
         if (table.interleaved) mla_rope_kernel<__nv_bfloat16, true><<<grid, threads, 0, stream>>>(p);
@@ -239,7 +238,6 @@ inline bool launch_rope(const mla_rope_dims& d, const mla_rope_table& table, con
         if (table.interleaved) mla_rope_kernel<float, true><<<grid, threads, 0, stream>>>(p);
         else mla_rope_kernel<float, false><<<grid, threads, 0, stream>>>(p);
     }
-    return true;
 }
 
 // ------------------------------------------------------------------ pool and books
@@ -525,22 +523,25 @@ inline void launch_append(const AppendParams& p, cudaStream_t stream) {
 }
 
 // ------------------------------------------------------------------ page moves
-constexpr int kSliceBytes = 2 * kMoveThreads * 16;  // of a page, per CTA: two loads in flight per thread
-inline int page_slices(int page_bytes) { return (page_bytes + kSliceBytes - 1) / kSliceBytes; }
+// A CTA moves slices of pages, two 16-byte loads in flight per thread; 288 threads cut
+// a page (36,864 or 73,728 bytes) into 4 or 8 whole slices.
+constexpr int kCopyThreads = 288;
+constexpr int kSliceBytes = 2 * kCopyThreads * 16;
+static_assert(kPage * kDqk % kSliceBytes == 0, "whole slices");
+inline int page_slices(int page_bytes) { return page_bytes / kSliceBytes; }
 
 __device__ __forceinline__ void copy_slice(const CachePool& pool, int src, int dst, int slice) {
     const uint8_t* s = pool.kv + (size_t)src * pool.page_bytes;
     uint8_t* d = pool.kv + (size_t)dst * pool.page_bytes;
-    const int a = slice * kSliceBytes + threadIdx.x * 16, b = a + kMoveThreads * 16;
-    uint4 va, vb;
-    if (a < pool.page_bytes) va = *reinterpret_cast<const uint4*>(s + a);
-    if (b < pool.page_bytes) vb = *reinterpret_cast<const uint4*>(s + b);
-    if (a < pool.page_bytes) *reinterpret_cast<uint4*>(d + a) = va;
-    if (b < pool.page_bytes) *reinterpret_cast<uint4*>(d + b) = vb;
+    const int a = slice * kSliceBytes + threadIdx.x * 16, b = a + kCopyThreads * 16;
+    const uint4 va = *reinterpret_cast<const uint4*>(s + a);
+    const uint4 vb = *reinterpret_cast<const uint4*>(s + b);
+    *reinterpret_cast<uint4*>(d + a) = va;
+    *reinterpret_cast<uint4*>(d + b) = vb;
     if (slice == 0 && threadIdx.x == 0 && pool.scales != nullptr) pool.scales[dst] = pool.scales[src];
 }
 
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kCopyThreads)
     mla_cache_copy_kernel(const CachePool pool, const int32_t* src, const int32_t* dst, int32_t* status) {
     const int s = src[blockIdx.x], d = dst[blockIdx.x];
     if (s < 0) return;
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(kMoveThreads)
 }
 inline void launch_copy_pages(const CachePool& pool, int n, const int32_t* src, const int32_t* dst, int32_t* status,
                               cudaStream_t stream) {
-    mla_cache_copy_kernel<<<dim3(n, page_slices(pool.page_bytes)), kMoveThreads, 0, stream>>>(pool, src, dst, status);
+    mla_cache_copy_kernel<<<dim3(n, page_slices(pool.page_bytes)), kCopyThreads, 0, stream>>>(pool, src, dst, status);
 }
 
 // The second kernel of a call, launched as a programmatic dependent of the first: its
@@ -562,7 +563,7 @@ template <typename... P, typename... A>
 inline void launch_after(void (*kernel)(P...), dim3 grid, cudaStream_t stream, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kMoveThreads);
+    cfg.blockDim = dim3(kCopyThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -667,7 +668,7 @@ __global__ void __launch_bounds__(kBookThreads)
 }
 
 // CTA (i, s): slice s of fork i's page, or (the last s) its table row.
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kCopyThreads)
     mla_cache_fork_kernel(const CacheBooks k, const CachePool pool, const int32_t* parents, const int32_t* children,
                           const int32_t* ws) {
     griddep_wait();  // the plan
@@ -678,7 +679,7 @@ __global__ void __launch_bounds__(kMoveThreads)
     } else {
         const int parent = parents[blockIdx.x], child = children[blockIdx.x];
         const int full = k.lens[child] / kPage;
-        for (int j = threadIdx.x; j < full; j += kMoveThreads) {
+        for (int j = threadIdx.x; j < full; j += kCopyThreads) {
             const int page = k.bt[(size_t)parent * k.max_blocks + j];
             k.bt[(size_t)child * k.max_blocks + j] = page;
             if ((unsigned)page >= (unsigned)k.num_blocks) raise(k.status, MLA_STATUS_BAD_BLOCK_TABLE);
@@ -800,26 +801,42 @@ __global__ void __launch_bounds__(kBookThreads) mla_cache_compact_plan_kernel(co
     }
 }
 
-__global__ void __launch_bounds__(kMoveThreads)
-    mla_cache_compact_kernel(const CacheBooks k, const CachePool pool, const int32_t* ws, int slices) {
+__global__ void __launch_bounds__(kCopyThreads)
+    mla_cache_compact_kernel(const CacheBooks k, const CachePool pool, const int32_t* ws, int shift) {
     griddep_wait();  // the plan
     const int live = ws[kCompactLive], moves = ws[kCompactMoves];
     const int32_t* list = ws + kCompactList;
     const int32_t* place = list + k.num_blocks;
-    const int64_t units = (int64_t)moves * slices;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int m = (int)(u / slices), s = (int)(u - (int64_t)m * slices);
-        const int dst = list[m], src = list[moves + m];
+    // A unit is move u >> shift, slice u & (slices - 1) of its 4 or 8; the next unit's pages
+    // are looked up while this one's bytes are on their way.
+    const int64_t units = (int64_t)moves << shift;
+    int64_t u = blockIdx.x;
+    int dst = 0, src = 0;
+    if (u < units) {
+        dst = list[u >> shift];
+        src = list[moves + (u >> shift)];
+    }
+    while (u < units) {
+        const int64_t next = u + gridDim.x;
+        int dst2 = 0, src2 = 0;
+        if (next < units) {
+            dst2 = list[next >> shift];
+            src2 = list[moves + (next >> shift)];
+        }
+        const int s = (int)(u & ((1 << shift) - 1));
         copy_slice(pool, src, dst, s);
         if (s == 0 && threadIdx.x == 0) {
             k.refs[dst] = k.refs[src];
             k.refs[src] = 0;
         }
+        u = next;
+        dst = dst2;
+        src = src2;
     }
     for (int b = blockIdx.x; b < k.batch; b += gridDim.x) {
         const int pages = pages_of(clamp_seqlen(k.lens[b], k.max_blocks));
         int32_t* bt = k.bt + (size_t)b * k.max_blocks;
-        for (int j = threadIdx.x; j < pages; j += kMoveThreads) {
+        for (int j = threadIdx.x; j < pages; j += kCopyThreads) {
             const int page = bt[j];
             if ((unsigned)page >= (unsigned)k.num_blocks) {
                 raise(k.status, MLA_STATUS_BAD_BLOCK_TABLE);
@@ -837,7 +854,7 @@ inline void launch_compact(const CacheBooks& k, const CachePool& pool, int32_t* 
     mla_cache_compact_plan_kernel<<<1, kBookThreads, 0, stream>>>(k, ws);
     const int64_t most = max((int64_t)k.batch, (int64_t)(k.num_blocks / 2) * slices);
     launch_after(mla_cache_compact_kernel, dim3((unsigned)min((int64_t)148 * 16, max(most, (int64_t)1))), stream, k, pool,
-                 (const int32_t*)ws, slices);
+                 (const int32_t*)ws, slices == 4 ? 2 : 3);
 }
 
 }  // namespace mla

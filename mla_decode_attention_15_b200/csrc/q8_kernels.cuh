@@ -63,7 +63,7 @@ constexpr float kQ8Grow = 4.8f;
 // The Q warps wait for most of an item; they leave the issue slots alone meanwhile.
 constexpr int kQ8Nap = 200, kQ8MaxNaps = 1 << 22;  // ns; about a second
 constexpr float kQ8MinBias = -60.0f;
-constexpr float kQ8Unset = -1e30f;              // running max before the first visible token
+constexpr float kQ8Unset = -3.402823466e38f;    // running max before the first visible token: below every score
 
 struct Q8Params : FwdParams {
     const __nv_bfloat16* q;   // [B * N][576]

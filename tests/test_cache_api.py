@@ -77,7 +77,7 @@ def _rope_rc(lib, ptrs=(0x1000, 0x2000, 0x3000), **kw):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(tokens=-1), BAD), (dict(num_heads=0), BAD), (dict(width=56), BAD), (dict(width=196), BAD), (dict(offset=4), BAD),
+    (dict(tokens=-1), BAD), (dict(num_heads=0), BAD), (dict(num_heads=65536), BAD), (dict(width=2056), BAD), (dict(width=56), BAD), (dict(width=196), BAD), (dict(offset=4), BAD),
     (dict(offset=136), BAD), (dict(offset=-8), BAD), (dict(width=65544), BAD), (dict(transpose=2), BAD), (dict(dtype=2), UNSUP),
     (dict(x_token_stride=385), BAD), (dict(x_head_stride=-192), BAD),
     (dict(out_head_stride=184), BAD), (dict(out_token_stride=376), BAD), (dict(out_token_stride=0), BAD)])
@@ -164,7 +164,9 @@ def test_cache_counts_and_strides(lib):
         assert lib.mla_cache_append(d, T, P[0], cs, P[1], ps, P[2], None, P[3], P[4], P[5], P[6], None, None) == BAD
     assert lib.mla_cache_append(d, 0, None, 512, None, 64, P[2], None, P[3], P[4], P[5], P[6], None, None) == OK
     assert lib.mla_cache_compact_workspace_bytes(ctypes.byref(_cache_dims(num_blocks=0))) == 0
-    assert lib.mla_cache_compact_workspace_bytes(d) == 4 * (4 + 16)
+    # (what the Python wrappers allocate)
+    assert lib.mla_cache_compact_workspace_bytes(d) == 16 + 8 * 8
+    assert [lib.mla_cache_fork_workspace_bytes(n) for n in (1, 7, 1024)] == [12, 84, 12288]
 
 
 def _q8_rc(lib, d, p):

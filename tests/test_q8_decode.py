@@ -236,6 +236,29 @@ def test_scores_that_rise_along_the_sequence(dev):
         check(d, out, lse, False)
 
 
+@pytest.mark.parametrize("scale", [1e30, 1e34, -1e30])
+def test_scores_of_any_size(dev, scale):
+    """Scores near the ends of fp32: one token takes all the weight, and scores far below zero are
+    still scores.  The weight 1 is exact, so the row comes out exactly but for the division."""
+    d = build([3, 200, 64], 1, 16, seed=24)
+    d["q"] = -d["q"].abs()
+    d["kv"] = d["kv"].float().abs().to(torch.float8_e4m3fn)
+    g = {k: v.to(dev) for k, v in d.items()}
+    dec = ca.Q8Decoder(3, 1, 16, d["kv"].shape[0], d["bt"].shape[1], False, 2, dev, fp32_out=True, inline_plan=True)
+    dec.plan(g["lens"])
+    out, lse = dec(g["q"], g["kv"], g["scales"], g["bt"], g["lens"], scale)
+    torch.cuda.synchronize()
+    assert dec.status() == 0 and bool(torch.isfinite(lse).all())
+    kv = wide(d).double()
+    for b, L in enumerate([3, 200, 64]):
+        k = kv[d["bt"][b, :(L + 63) // 64].long()].reshape(-1, 576)[:L]
+        z = d["q"][b, 0].double() @ k.T * scale
+        best, at = z.max(-1)
+        assert bool(((lse[b, :, 0].cpu().double() - best).abs() <= 2.0 ** -13 * best.abs()).all())
+        ref = k[at, :512]
+        assert bool(((out[b, 0].cpu().double() - ref).abs() <= 2.0 ** -20 * ref.abs()).all())
+
+
 def test_same_bits_again_and_on_another_stream(dev):
     d = build([5000, 3, 4097, 64], 2, 16, seed=16)
     a = run(d, dev, True, True)
