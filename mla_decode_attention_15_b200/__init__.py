@@ -47,6 +47,7 @@ from .binding import (  # noqa: F401
 )
 from .cache import (  # noqa: F401
     Q8Decoder,
+    absorbed_mla_step,
     cache_append,
     cache_compact,
     cache_compact_workspace,

@@ -454,3 +454,39 @@ class Q8Decoder:
 
     def status(self) -> int:
         return bd.mla_decode_get_status(self.schedule)
+
+
+# ---------------------------------------------------------------- one layer's step
+def absorbed_mla_step(q_in: torch.Tensor, c_kv: torch.Tensor, k_pe: torch.Tensor, positions: torch.Tensor,
+                      new_offsets: torch.Tensor, w_uk: torch.Tensor, w_uv: torch.Tensor, rope: mla_rope_table,
+                      block_table: torch.Tensor, cache_seqlens: torch.Tensor, kv_cache: torch.Tensor,
+                      kv_scales: Optional[torch.Tensor], softmax_scale: float, decoder,
+                      status: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """One absorbed-MLA decode step for one layer, from the projections' outputs:
+    the queries' RoPE part is rotated, the new rows are written into the cache,
+    and ``absorbed_mla_decode`` follows over the cache as it then is.
+
+    q_in [B, s_q, h, 192] (each head's 128-wide part, then its RoPE part), c_kv
+    [B * s_q, 512] and k_pe [B * s_q, 64]: the new tokens' rows, request by request;
+    positions [B * s_q] int32: theirs in their requests; new_offsets [B + 1] int32: 0,
+    s_q, 2 s_q, ...; cache_seqlens counts the new rows.  ``decoder`` is a planned
+    MlaDecoder for a bf16 cache (kv_scales None), or a Q8Decoder.  Returns (out
+    [B, s_q, h, 128] bf16, lse [B, h, s_q])."""
+    if isinstance(stream, torch.cuda.Stream):
+        # (what the step allocates then belongs to that stream)
+        with torch.cuda.stream(stream):
+            return absorbed_mla_step(q_in, c_kv, k_pe, positions, new_offsets, w_uk, w_uv, rope, block_table, cache_seqlens,
+                                     kv_cache, kv_scales, softmax_scale, decoder, status)
+    if stream is not None:
+        _fail("stream must be a torch.cuda.Stream")
+    if q_in.dim() != 4:
+        _fail("q_in must be [B, s_q, h, 192]")
+    B, s_q, h, width = q_in.shape
+    q = rope_apply(q_in.reshape(B * s_q, h, width), positions, rope, offset=bd.ABSORB_D_NOPE).view(q_in.shape)
+    cache_append(c_kv, k_pe, new_offsets, block_table, cache_seqlens, kv_cache, kv_scales, rope, status)
+    q_lat = bd.absorb_q(q, w_uk)
+    if kv_scales is None:
+        o_lat, lse = decoder(q_lat, kv_cache, block_table, cache_seqlens, softmax_scale)
+    else:
+        o_lat, lse = decoder(q_lat, kv_cache, kv_scales, block_table, cache_seqlens, softmax_scale)
+    return bd.absorb_o(o_lat, w_uv), lse

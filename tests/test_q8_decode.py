@@ -461,3 +461,62 @@ def test_append_fork_decode_compact_together(dev):
     ca.cache_compact(bt, lens, refs, kv, scales, status=status)
     assert int((refs > 0).sum()) == int((before > 0).sum()) and not refs[int((before > 0).sum()):].any()
     attend()
+
+
+@pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("inline", [True, False])
+@pytest.mark.parametrize("s_q,h", [(1, 16), (2, 128)])
+def test_absorbed_step_is_its_parts(dev, s_q, h, inline, q8):
+    """A layer's step: the same bits as its parts called one by one with the device drained between
+    them, three steps in a row on one stream, into caches of either form; the new rows
+    are the ones the decode sees."""
+    B, nb, steps = 4, 24, 3
+    g = torch.Generator().manual_seed(40 + h)
+    r = lambda *s: (torch.randn(*s, generator=g)).bfloat16().to(dev)  # noqa: E731
+    rope = ca.make_rope(scaling="yarn", factor=40.0)
+    w_uk, w_uv = r(h, 128, 512) / 11, r(h, 512, 128) / 22
+    lens0 = [0, 63, 64, 200]
+    bt = torch.randperm(nb, generator=g).int().view(B, 6).contiguous().to(dev)
+    off = (torch.arange(B + 1, dtype=torch.int32) * s_q).to(dev)
+    pools = []
+    for _ in range(2):
+        d = build([64], 1, 1, seed=41, spare=nb - 1)
+        kv = (d["kv"] if q8 else wide(d)).to(dev)
+        pools.append((kv, d["scales"].to(dev) if q8 else None))
+    ins = [(r(B, s_q, h, 192), r(B * s_q, 576)) for _ in range(steps)]
+    make = (lambda: ca.Q8Decoder(B, s_q, h, nb, 6, s_q > 1, 0, dev, inline_plan=inline)) if q8 else \
+        (lambda: bd.MlaDecoder(B, s_q, h, nb, 6, s_q > 1, 0, dev, inline_plan=inline))
+    a, b = make(), make()
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    lens = [torch.tensor([n + s_q * (i + 1) for n in lens0], dtype=torch.int32, device=dev) for i in range(steps)]
+    pos = [(x[:, None] - s_q + torch.arange(s_q, device=dev, dtype=torch.int32)).flatten().contiguous() for x in lens]
+    torch.cuda.synchronize()
+    got = []
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    for i, (q, kv) in enumerate(ins):
+        a.plan(lens[i], stream)
+        out, lse = ca.absorbed_mla_step(q, kv[:, :512], kv[:, 512:], pos[i], off, w_uk, w_uv, rope, bt, lens[i], *pools[0], SCALE, a,
+                                        status, stream)
+        with torch.cuda.stream(stream):
+            got.append((out, lse.clone()))
+    stream.synchronize()
+    assert a.status() == 0 and int(status) == 0
+    for i, (q, kv) in enumerate(ins):
+        b.plan(lens[i])
+        torch.cuda.synchronize()
+        qr = ca.rope_apply(q.view(B * s_q, h, 192), pos[i], rope, offset=128).view(q.shape)
+        torch.cuda.synchronize()
+        ca.cache_append(kv[:, :512], kv[:, 512:], off, bt, lens[i], *pools[1], rope=rope)
+        torch.cuda.synchronize()
+        ql = bd.absorb_q(qr, w_uk)
+        torch.cuda.synchronize()
+        o, lse = b(ql, *(x for x in pools[1] if x is not None), bt, lens[i], SCALE)
+        torch.cuda.synchronize()
+        assert torch.equal(lse, got[i][1])
+        assert torch.equal(bd.absorb_o(o, w_uv), got[i][0])
+    assert torch.equal(pools[0][0].view(torch.uint8), pools[1][0].view(torch.uint8))
+    d = dict(q=ql.cpu(), bt=bt.cpu(), lens=lens[-1].cpu())
+    pool = wide(dict(kv=pools[1][0].cpu(), scales=pools[1][1].cpu())) if q8 else pools[1][0].cpu()
+    ref, rl = oracle.mla_oracle_fwd(d["q"], pool, d["bt"], d["lens"], SCALE, causal=s_q > 1)
+    helpers.compare(o, lse, ref, rl)
