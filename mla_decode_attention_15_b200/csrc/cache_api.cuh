@@ -17,13 +17,14 @@ int make_plan_q8(const mla_decode_dims* d, Plan* pl) {
     pl->gr.N = d->num_heads * d->s_q;
     pl->gr.NG = pl->gr.N <= 16 ? 16 : 32;
     pl->gr.Hg = (pl->gr.N + pl->gr.NG - 1) / pl->gr.NG;
-    if ((int64_t)d->batch * pl->gr.Hg * ((int64_t)d->max_blocks_per_seq + kItemOverhead) >= (int64_t)INT32_MAX)
+    if ((int64_t)d->batch * pl->gr.Hg * ((int64_t)d->max_blocks_per_seq + kQ8ItemOverhead) >= (int64_t)INT32_MAX)
         return MLA_ERR_UNSUPPORTED;
     int sms = 0;
     rc = resolve_ctas(d, &sms);
     if (rc != MLA_OK) return rc;
     pl->pair = false;
     pl->shift = kPageShift;
+    pl->overhead = kQ8ItemOverhead;
     if (pl->gr.Hg > 1 && sms >= pl->gr.Hg) {
         pl->G = sms / pl->gr.Hg;
         pl->BG = d->batch;
@@ -223,6 +224,7 @@ int mla_decode_q8_fwd(const mla_decode_dims* dims, void* schedule, void* workspa
     p.BG = pl.BG;
     p.Hg = pl.plan_Hg;
     p.share = pl.share;
+    p.overhead = pl.overhead;
     p.slots_cap = (int)pl.slots;
     p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
     p.test_stall = (dims->flags & MLA_FLAG_TEST_STALL) ? 1 : 0;

@@ -259,6 +259,7 @@ struct FwdParams {
     // head group (1: none; >1: the plan has one row per request and CTA c
     // walks range c / share for head group c % share).
     int share;
+    int overhead;      // units charged per work item of the plan
     int out_f32;       // MLA_FLAG_FP32_OUT: final rows are written as fp32
     float scale_log2;  // softmax_scale * log2(e)
     int test_stall;    // MLA_FLAG_TEST_STALL: leave the first page unloaded
@@ -1320,7 +1321,7 @@ __device__ void build_plan_in_cta(const FwdParams& p, int32_t* scratch, int32_t*
         if (bg < BG) {
             const int L = __ldg(p.seqlens + bg / Hg);
             any_bad |= !seqlen_in_range(L, mb);
-            v = (int)units_of(blocks_of(clamp_seqlen(L, mb), kPageShift));
+            v = (int)units_of(blocks_of(clamp_seqlen(L, mb), kPageShift), p.overhead);
         }
         int x = v;
 #pragma unroll
@@ -1346,7 +1347,7 @@ __device__ void build_plan_in_cta(const FwdParams& p, int32_t* scratch, int32_t*
     __syncthreads();
     if (tid == 0) {
         const int64_t T = units_per_cta(W, G);
-        cta_meta(prefix, BG, W, T, k, plan_s);
+        cta_meta(prefix, BG, W, T, k, plan_s, p.overhead);
         plan_s[kPlanW] = (int)W;
         plan_s[kPlanT] = (int)T;
     }
@@ -1366,13 +1367,13 @@ __device__ void publish_plan_in_cta(const FwdParams& p, int NG, const int32_t* s
     int32_t* bginfo = p.plan_out + bg_offset_words(G);
     int my_slots = 0;
     for (int bg = tid; bg < BG; bg += nthr) {
-        const int P = pages_in_prefix(prefix, bg);
-        const int ns = num_splits_of(prefix, bg, P, T);
+        const int P = pages_in_prefix(prefix, bg, p.overhead);
+        const int ns = num_splits_of(prefix, bg, P, T, p.overhead);
         if (ns > 1) my_slots += ns;
-        int owner = P > 0 ? first_cta_of(prefix, bg, T) : 0;
+        int owner = P > 0 ? first_cta_of(prefix, bg, T, p.overhead) : 0;
         if (owner > G - 1) owner = G - 1;
         if (owner == k && writer) {
-            bginfo[kBgWords * bg] = ns > 1 ? first_split_slot(prefix, bg, T) : 0;
+            bginfo[kBgWords * bg] = ns > 1 ? first_split_slot(prefix, bg, T, p.overhead) : 0;
             bginfo[kBgWords * bg + 1] = ns;
         }
     }
@@ -1805,7 +1806,7 @@ __global__ void __launch_bounds__(kDv / 4) mla_decode_combine_kernel(const Combi
 // prefix is also written to the schedule buffer.
 __global__ void __launch_bounds__(1024)
     mla_decode_schedule_kernel(const int32_t* __restrict__ seqlens_g, int32_t* __restrict__ sched, int B,
-                               int Hg, int NG, int G, int max_blocks, int use_smem, int shift, int share_hg) {
+                               int Hg, int NG, int G, int max_blocks, int use_smem, int shift, int share_hg, int ov) {
     extern __shared__ int32_t sh[];
     __shared__ int warp_tot[32];
     __shared__ int carry;
@@ -1836,7 +1837,7 @@ __global__ void __launch_bounds__(1024)
         if (bg < BG) {
             const int L = seqlens[bg / Hg];
             if (!seqlen_in_range(L, max_blocks)) bad_len = 1;
-            v = (int)units_of(blocks_of(clamp_seqlen(L, max_blocks), shift));
+            v = (int)units_of(blocks_of(clamp_seqlen(L, max_blocks), shift), ov);
         }
         const int incl = block_inclusive_scan(v, warp_tot);
         if (bg < BG) {
@@ -1854,19 +1855,19 @@ __global__ void __launch_bounds__(1024)
     }
     __syncthreads();
     const int64_t T = units_per_cta(W, G);
-    for (int k = threadIdx.x; k < G; k += 1024) cta_meta(prefix, BG, W, T, k, meta + (size_t)k * kMetaWords);
+    for (int k = threadIdx.x; k < G; k += 1024) cta_meta(prefix, BG, W, T, k, meta + (size_t)k * kMetaWords, ov);
     __syncthreads();
     if (threadIdx.x == 0) carry = 0;
     __syncthreads();
     for (int base = 0; base < BG; base += 1024) {
         const int bg = base + threadIdx.x;
         int ns = 0;
-        if (bg < BG) ns = num_splits_of(prefix, bg, pages_in_prefix(prefix, bg), T);
+        if (bg < BG) ns = num_splits_of(prefix, bg, pages_in_prefix(prefix, bg, ov), T, ov);
         const int v = ns > 1 ? ns : 0;
         const int incl = block_inclusive_scan(v, warp_tot);
         if (bg < BG) {
             // one-CTA kernels (64-token units): fixed slots; CTA-pair plans: running count
-            bginfo[kBgWords * bg] = shift != kPageShift ? carry + incl - v : ns > 1 ? first_split_slot(prefix, bg, T) : 0;
+            bginfo[kBgWords * bg] = shift != kPageShift ? carry + incl - v : ns > 1 ? first_split_slot(prefix, bg, T, ov) : 0;
             bginfo[kBgWords * bg + 1] = ns;
         }
         __syncthreads();

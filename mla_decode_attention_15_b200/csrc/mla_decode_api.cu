@@ -79,6 +79,7 @@ struct Plan {
     int ctas;     // CTAs launched
     bool pair;    // CTA-pair kernel (query groups of 128 columns)
     int64_t slots;
+    int overhead = kItemOverhead;  // units charged per work item
 };
 
 // Clusters of the pair kernel that can be resident at once on the current
@@ -403,7 +404,7 @@ int launch_schedule(const Plan& pl, int batch, int max_blocks, const int32_t* ca
     const int use_smem = sh_bytes <= 48 * 1024 ? 1 : 0;
     mla_decode_schedule_kernel<<<1, 1024, use_smem ? sh_bytes : 0, stream>>>(
         cache_seqlens, static_cast<int32_t*>(schedule), batch, pl.plan_Hg, pl.gr.NG, pl.G, max_blocks, use_smem,
-        pl.shift, pl.share);
+        pl.shift, pl.share, pl.overhead);
     return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
@@ -537,15 +538,15 @@ void host_plan(const Plan& pl, int batch, int mb, const int32_t* seqlens, void* 
         const int L = seqlens[bg / Hg];
         if (!seqlen_in_range(L, mb)) bad_len = 1;
         prefix[bg] = (int32_t)W;
-        W += units_of(blocks_of(clamp_seqlen(L, mb), sh));
+        W += units_of(blocks_of(clamp_seqlen(L, mb), sh), pl.overhead);
     }
     prefix[BG] = (int32_t)W;
     const int64_t T = units_per_cta(W, G);
-    for (int k = 0; k < G; ++k) cta_meta(prefix, BG, W, T, k, s + kHdrWords + (size_t)k * kMetaWords);
+    for (int k = 0; k < G; ++k) cta_meta(prefix, BG, W, T, k, s + kHdrWords + (size_t)k * kMetaWords, pl.overhead);
     int64_t slots = 0;
     for (int bg = 0; bg < BG; ++bg) {
-        const int ns = num_splits_of(prefix, bg, pages_in_prefix(prefix, bg), T);
-        bginfo[kBgWords * bg] = pl.pair ? (int32_t)slots : ns > 1 ? first_split_slot(prefix, bg, T) : 0;
+        const int ns = num_splits_of(prefix, bg, pages_in_prefix(prefix, bg, pl.overhead), T, pl.overhead);
+        bginfo[kBgWords * bg] = pl.pair ? (int32_t)slots : ns > 1 ? first_split_slot(prefix, bg, T, pl.overhead) : 0;
         bginfo[kBgWords * bg + 1] = ns;
         if (ns > 1) slots += ns;
     }
@@ -661,6 +662,7 @@ int mla_decode_fwd(const mla_decode_dims* dims, void* schedule, void* workspace,
     p.BG = pl.BG;
     p.Hg = pl.pair ? pl.share : pl.gr.Hg;  // pair kernel: head groups walking each range
     p.share = 1;
+    p.overhead = pl.overhead;
     p.slots_cap = (int)pl.slots;
     p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
     p.test_stall = (dims->flags & MLA_FLAG_TEST_STALL) ? 1 : 0;
@@ -763,6 +765,7 @@ int mla_gqa_decode_fwd(const mla_gqa_dims* dims, void* schedule, void* workspace
     p.BG = pl.BG;
     p.Hg = pl.plan_Hg;
     p.share = pl.share;
+    p.overhead = pl.overhead;
     p.slots_cap = (int)pl.slots;
     p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
     p.test_stall = (dims->flags & MLA_FLAG_TEST_STALL) ? 1 : 0;

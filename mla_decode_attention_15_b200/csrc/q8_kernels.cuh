@@ -836,13 +836,13 @@ __device__ void q8_publish(const FwdParams& p, int NG, const int32_t* prefix, co
     int32_t* bginfo = p.plan_out + bg_offset_words(G);
     int slots = 0;
     for (int bg = lane; bg < BG; bg += 32) {
-        const int P = pages_in_prefix(prefix, bg);
-        const int ns = num_splits_of(prefix, bg, P, T);
+        const int P = pages_in_prefix(prefix, bg, p.overhead);
+        const int ns = num_splits_of(prefix, bg, P, T, p.overhead);
         if (ns > 1) slots += ns;
-        int owner = P > 0 ? first_cta_of(prefix, bg, T) : 0;
+        int owner = P > 0 ? first_cta_of(prefix, bg, T, p.overhead) : 0;
         if (owner > G - 1) owner = G - 1;
         if (owner == k && writer) {
-            bginfo[kBgWords * bg] = ns > 1 ? first_split_slot(prefix, bg, T) : 0;
+            bginfo[kBgWords * bg] = ns > 1 ? first_split_slot(prefix, bg, T, p.overhead) : 0;
             bginfo[kBgWords * bg + 1] = ns;
         }
     }

@@ -1,7 +1,7 @@
 // Split-KV work partitioning for the persistent decode kernel.
 //
 // Work units: request b, head group g ("bg" = b * Hg + g) owns
-//   units(bg) = P_b + kItemOverhead   (P_b = ceil(L_b / 2^shift) token blocks of
+//   units(bg) = P_b + overhead        (P_b = ceil(L_b / 2^shift) token blocks of
 //                                       2^shift tokens; 0 if P_b == 0)
 // The one-CTA kernels walk 64-token pages (shift 6).  The CTA-pair kernel walks
 // steps of 128 tokens (shift 7, two pages per step), and builds its plan over
@@ -34,6 +34,16 @@ constexpr int kStepShift = 7;      // CTA-pair kernel: units of two pages
 constexpr int kDqk = 576;
 constexpr int kDv = 512;
 constexpr int kItemOverhead = 1;   // units charged per (request, head group)
+// The 8-bit decode's pages are half the bytes, and its items cost more beside
+// them (the split of Q into two terms, the first step's wait for a maximum, a
+// longer epilogue), so a range with a second item in it weighs several pages.
+// Measured, event-timed us for 1 / 4 / 6 / 8 / 12 / 16 units: 16 requests x 2
+// tokens x 1-16K 43.8 / 40.6 / 39.5 / 39.3 / 42.2 / 42.6; 16 x 64K 125.6 / 123.8
+// / 121.4 / 121.2 / 121.5 / 124.9; 1 x 1K 13.9 / 12.3 / 12.2 / 12.1 / 12.0 / 12.0
+// (its 16 pages then start on even units, so that no range holds an odd page).
+// The functions below take the overhead as `ov`.  It may exceed a range: that
+// CTA's range is then empty.
+constexpr int kQ8ItemOverhead = 6;
 // Smallest range worth its own CTA.  Measured on B200 (graph-replayed steps):
 // with 1 instead of 2, bs1 x 1K (16 pages) spreads over 9 CTAs instead of 6 and
 // its decode kernel takes 16.4 instead of 18.4 us; no other workload changed.
@@ -115,7 +125,7 @@ __host__ __device__ inline bool seqlen_in_range(int L, int max_blocks) {
 __host__ __device__ inline int pages_of(int L) { return (L + kPage - 1) / kPage; }
 // blocks of 2^shift tokens covering L tokens
 __host__ __device__ inline int blocks_of(int L, int shift) { return (L + (1 << shift) - 1) >> shift; }
-__host__ __device__ inline int64_t units_of(int P) { return P > 0 ? (int64_t)P + kItemOverhead : 0; }
+__host__ __device__ inline int64_t units_of(int P, int ov = kItemOverhead) { return P > 0 ? (int64_t)P + ov : 0; }
 
 __host__ __device__ inline int64_t units_per_cta(int64_t W, int G) {
     int64_t T = (W + G - 1) / (G > 0 ? G : 1);
@@ -134,24 +144,24 @@ __host__ __device__ inline int find_bg(const int32_t* prefix, int BG, int64_t u)
 }
 
 // Blocks of request-group bg (of its length clamped to the block table),
-// read back from the unit prefix: its units are P + kItemOverhead, or 0 when
+// read back from the unit prefix: its units are P + ov, or 0 when
 // P == 0.  No access to the lengths.
-__host__ __device__ inline int pages_in_prefix(const int32_t* prefix, int bg) {
+__host__ __device__ inline int pages_in_prefix(const int32_t* prefix, int bg, int ov = kItemOverhead) {
     const int units = prefix[bg + 1] - prefix[bg];
-    return units > 0 ? units - kItemOverhead : 0;
+    return units > 0 ? units - ov : 0;
 }
 
 // (bg, page) position of unit u; u >= W maps to (BG, 0).
 __host__ __device__ inline void locate_unit(const int32_t* prefix, int BG, int64_t W, int64_t u, int* bg_out,
-                                            int* page_out) {
+                                            int* page_out, int ov = kItemOverhead) {
     if (u >= W) {
         *bg_out = BG;
         *page_out = 0;
         return;
     }
     int bg = find_bg(prefix, BG, u);
-    int P = pages_in_prefix(prefix, bg);
-    int64_t p = u - (int64_t)prefix[bg] - kItemOverhead;
+    int P = pages_in_prefix(prefix, bg, ov);
+    int64_t p = u - (int64_t)prefix[bg] - ov;
     if (p < 0) p = 0;
     if (p > P) p = P;
     *bg_out = bg;
@@ -159,32 +169,32 @@ __host__ __device__ inline void locate_unit(const int32_t* prefix, int BG, int64
 }
 
 // First / last CTA that owns a page of bg (P > 0).
-__host__ __device__ inline int first_cta_of(const int32_t* prefix, int bg, int64_t T) {
-    return (int)(((int64_t)prefix[bg] + kItemOverhead) / T);
+__host__ __device__ inline int first_cta_of(const int32_t* prefix, int bg, int64_t T, int ov = kItemOverhead) {
+    return (int)(((int64_t)prefix[bg] + ov) / T);
 }
-__host__ __device__ inline int last_cta_of(const int32_t* prefix, int bg, int P, int64_t T) {
-    return (int)(((int64_t)prefix[bg] + kItemOverhead + P - 1) / T);
+__host__ __device__ inline int last_cta_of(const int32_t* prefix, int bg, int P, int64_t T, int ov = kItemOverhead) {
+    return (int)(((int64_t)prefix[bg] + ov + P - 1) / T);
 }
 
-__host__ __device__ inline int num_splits_of(const int32_t* prefix, int bg, int P, int64_t T) {
-    return P > 0 ? last_cta_of(prefix, bg, P, T) - first_cta_of(prefix, bg, T) + 1 : 0;
+__host__ __device__ inline int num_splits_of(const int32_t* prefix, int bg, int P, int64_t T, int ov = kItemOverhead) {
+    return P > 0 ? last_cta_of(prefix, bg, P, T, ov) - first_cta_of(prefix, bg, T, ov) + 1 : 0;
 }
 
 // Work range of CTA k: units [k*T, min((k+1)*T, W)).
 __host__ __device__ inline void cta_meta(const int32_t* prefix, int BG, int64_t W, int64_t T, int k,
-                                         int32_t* meta) {
+                                         int32_t* meta, int ov = kItemOverhead) {
     int64_t u0 = (int64_t)k * T;
     int64_t u1 = u0 + T;
     if (u0 > W) u0 = W;
     if (u1 > W) u1 = W;
     int bb, bp, eb, ep;
-    locate_unit(prefix, BG, W, u0, &bb, &bp);
-    locate_unit(prefix, BG, W, u1, &eb, &ep);
+    locate_unit(prefix, BG, W, u0, &bb, &bp, ov);
+    locate_unit(prefix, BG, W, u1, &eb, &ep, ov);
     int first_split = 0;
     if (bb < BG) {
-        int P = pages_in_prefix(prefix, bb);
+        int P = pages_in_prefix(prefix, bb, ov);
         if (P > 0) {
-            first_split = k - first_cta_of(prefix, bb, T);
+            first_split = k - first_cta_of(prefix, bb, T, ov);
             if (first_split < 0) first_split = 0;
         }
     }
@@ -209,8 +219,8 @@ __host__ __device__ inline int64_t max_slots(int G) { return 2 * (int64_t)G; }
 // (CTA-pair plans, whose head groups share each range, number their slots
 // (base + split) * groups + group, with base a running count over requests.)
 __host__ __device__ inline int cta_slot(int k, bool first_item) { return 2 * k + (first_item ? 0 : 1); }
-__host__ __device__ inline int first_split_slot(const int32_t* prefix, int bg, int64_t T) {
-    const int c0 = first_cta_of(prefix, bg, T);
+__host__ __device__ inline int first_split_slot(const int32_t* prefix, int bg, int64_t T, int ov = kItemOverhead) {
+    const int c0 = first_cta_of(prefix, bg, T, ov);
     return cta_slot(c0, (int64_t)c0 * T >= (int64_t)prefix[bg]);
 }
 __host__ __device__ inline int64_t split_slot(int slot0, int i) {

@@ -220,6 +220,33 @@ def test_q8_host_plan_covers_every_page_once(lib, h, s_q, G, share):
     assert len(seen) == sum((int(n) + 63) // 64 for n in lens)
 
 
+@pytest.mark.parametrize("G", [1, 2, 7, 32, 148])
+def test_q8_host_plan_of_ragged_batches(lib, G):
+    """Ranges that fall inside an item's overhead are empty and belong to no split."""
+    g = torch.Generator().manual_seed(G)
+    for trial in range(40):
+        B = int(torch.randint(1, 60, (1,), generator=g))
+        lens = torch.randint(0, (65, 300, 5120)[trial % 3], (B,), generator=g, dtype=torch.int32)
+        d = _dd(batch=B, num_heads=16, max_blocks_per_seq=80, num_sms=G)
+        buf = torch.zeros(ca.mla_decode_q8_schedule_bytes(d), dtype=torch.uint8)
+        ca.mla_decode_q8_get_schedule_host(d, lens, buf)
+        hdr, meta, bginfo, prefix = helpers.read_plan(buf.numpy(), G, B)
+        pieces, seen = {}, set()
+        for items in helpers.walk_plan(meta, bginfo, lens, 1, 80):
+            for bg, p0, p1, unsplit, slot in items:
+                if p1 > p0:
+                    pieces.setdefault(bg, []).append((p0, p1, slot))
+                    assert unsplit or slot not in seen and 0 <= slot < 2 * G
+                    seen |= set() if unsplit else {slot}
+        for b, n in enumerate(lens.tolist()):
+            got = sorted(pieces.get(b, []))
+            assert [x for p0, p1, _ in got for x in range(p0, p1)] == list(range((n + 63) // 64))
+            assert int(bginfo[b][1]) == len(got)
+            s0 = int(bginfo[b][0])
+            if len(got) > 1:   # the slots the combine kernel reads
+                assert [s for _, _, s in got] == [s0] + [2 * ((s0 >> 1) + i) for i in range(1, len(got))]
+
+
 def test_python_wrappers_check_shapes(lib):
     kv = torch.zeros(4, 64, 1, 576, dtype=torch.float8_e4m3fn)
     sc = torch.ones(4, 1)
