@@ -329,6 +329,15 @@ __device__ __forceinline__ uint2 quant8(const float (&f)[8], float inv) {
     for (int e = 0; e < 4; ++e) w[e] = e4m3x2(finite_or_nan(f[2 * e] * inv), finite_or_nan(f[2 * e + 1] * inv));
     return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
+// The same of eight finite bf16 values (a finite value times a power of two that
+// brings the largest to 448 stays finite).
+__device__ __forceinline__ uint2 quant8_finite(const uint4& v, float inv) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = e4m3x2(__uint_as_float(w[e] << 16) * inv, __uint_as_float(w[e] & 0xffff0000u) * inv);
+    return make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
+}
 __device__ __forceinline__ uint32_t amax_of(uint32_t amax, float x) {
     const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
     return b < kInfBits ? max(amax, b) : amax;
@@ -420,17 +429,18 @@ __global__ void __launch_bounds__(kAppendThreads, 2) mla_cache_append_kernel(con
         }
     }
     float inv = 1.f;
+    bool finite = true;
     if constexpr (kQ8) {
         // Largest magnitude as bits, non-finite values included: they are the
         // largest, and where there is none the finite maximum is at hand.
-        uint32_t top = 0;
+        uint32_t two = 0;  // of the low and the high halves
 #pragma unroll
         for (int k = 0; k < kLatRows; ++k) {
             if (r0 + lr + 8 * k >= r1) continue;
-            const uint32_t w[4] = {lat[k].x, lat[k].y, lat[k].z, lat[k].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top = max(top, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+            two = __vmaxu2(two, __vmaxu2(__vmaxu2(lat[k].x & 0x7fff7fffu, lat[k].y & 0x7fff7fffu),
+                                         __vmaxu2(lat[k].z & 0x7fff7fffu, lat[k].w & 0x7fff7fffu)));
         }
+        uint32_t top = max(two << 16, two & 0xffff0000u);
         if (rr < r1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(pe[i]) & 0x7fffffffu);
@@ -441,7 +451,8 @@ __global__ void __launch_bounds__(kAppendThreads, 2) mla_cache_append_kernel(con
         uint32_t amax = 0;
 #pragma unroll
         for (int w = 0; w < kAppendThreads / 32; ++w) amax = max(amax, warp_max[w]);
-        if (amax >= kInfBits) {  // (seldom: some value is not finite)
+        finite = amax < kInfBits;
+        if (!finite) {  // (seldom)
             uint32_t fin = 0;
             for (int k = 0; k < kLatRows; ++k) {
                 if (r0 + lr + 8 * k >= r1) continue;
@@ -484,9 +495,15 @@ __global__ void __launch_bounds__(kAppendThreads, 2) mla_cache_append_kernel(con
         const int r = r0 + lr + 8 * k;
         if (r >= r1) continue;
         if constexpr (kQ8) {
-            float f[8];
-            unpack8(lat[k], f);
-            *reinterpret_cast<uint2*>(dst + r * kDqk + lc * 8) = quant8(f, inv);
+            uint2 v;
+            if (finite) {
+                v = quant8_finite(lat[k], inv);
+            } else {
+                float f[8];
+                unpack8(lat[k], f);
+                v = quant8(f, inv);
+            }
+            *reinterpret_cast<uint2*>(dst + r * kDqk + lc * 8) = v;
         } else {
             *reinterpret_cast<uint4*>(dst + (r * kDqk + lc * 8) * 2) = lat[k];
         }
