@@ -347,6 +347,10 @@ __device__ __forceinline__ uint32_t amax_of(uint32_t amax, float x) {
 // kLatRows pieces of 8 latent columns and 4 RoPE pairs for a full page; two such CTAs
 // fit an SM), so the scale costs no second read of them.  The CTA finds its
 // (request, page) by a scan over the requests' page counts.
+// A single token per request is a chain of dependent reads (offsets and lengths,
+// table, row) and the fence: 128 requests 5.4 us on B200.  Prompts are bound by the two
+// rounds of CTAs and by the conversions: 32,900 rows to e4m3 (57 MB read and written) 16.4 us,
+// of it the angles 2 us and the fence 1.2; 18.4 us with a check per value.
 constexpr int kAppendThreads = 512;
 constexpr int kLatRows = kPage * (kDv / 8) / kAppendThreads;  // 8
 static_assert(kPage * 8 == kAppendThreads, "one RoPE unit per thread");
@@ -541,7 +545,8 @@ inline void launch_append(const AppendParams& p, cudaStream_t stream) {
 
 // ------------------------------------------------------------------ page moves
 // A CTA moves slices of pages, two 16-byte loads in flight per thread; 288 threads cut
-// a page (36,864 or 73,728 bytes) into 4 or 8 whole slices.
+// a page (36,864 or 73,728 bytes) into 4 or 8 whole slices.  Bound by the bytes, each
+// read and written once; a compaction that moves 182 MB takes 31 us (5.9 TB/s).
 constexpr int kCopyThreads = 288;
 constexpr int kSliceBytes = 2 * kCopyThreads * 16;
 static_assert(kPage * kDqk % kSliceBytes == 0, "whole slices");
@@ -599,7 +604,9 @@ enum ForkWord { kForkOk = 0, kForkSrc = 1, kForkDst = 2, kForkWords = 3 };
 __host__ __device__ inline size_t fork_workspace_words(int n) { return (size_t)kForkWords * n; }
 
 // One CTA decides every fork, in order: checks the rows, ranks the forks that need
-// a page and hands them the lowest free ones.
+// a page and hands them the lowest free ones.  Which pages are free depends on every
+// fork before, so one block settles it; a chain of short reads and block scans, 6 us on B200 for
+// 24 forks in 350 pages and 8 us for 192 in 5,200, while the copy kernel is being launched.
 __global__ void __launch_bounds__(kBookThreads)
     mla_cache_fork_plan_kernel(const CacheBooks k, int n, const int32_t* parents, const int32_t* children, int32_t* ws) {
     __shared__ __align__(16) int child_s[kForkMax];
@@ -684,7 +691,8 @@ __global__ void __launch_bounds__(kBookThreads)
     }
 }
 
-// CTA (i, s): slice s of fork i's page, or (the last s) its table row.
+// CTA (i, s): slice s of fork i's page, or (the last s) its table row.  4.5 us for 24
+// forks of e4m3 pages, 8 us for 192 of bf16 pages (28 MB).
 __global__ void __launch_bounds__(kCopyThreads)
     mla_cache_fork_kernel(const CacheBooks k, const CachePool pool, const int32_t* parents, const int32_t* children,
                           const int32_t* ws) {
@@ -713,6 +721,8 @@ inline void launch_fork(const CacheBooks& k, const CachePool& pool, int n, const
 }
 
 // ------------------------------------------------------------------ free
+// A CTA per row: one counter per page, returned by atomics (whole numbers, so their
+// order does not matter).  Bound by the launch: 24 rows 5.5 us.
 __global__ void __launch_bounds__(kMoveThreads) mla_cache_free_kernel(const CacheBooks k, const int32_t* rows) {
     __shared__ int len;
     const int row = rows[blockIdx.x];
@@ -753,7 +763,8 @@ inline size_t compact_workspace_words(int num_blocks) { return kCompactList + 2 
 // pages that move or are moved to numbers both lists.  A warp owns a run of
 // consecutive pages, 32 at a time, and a lane keeps which of its pages are in use as
 // bits, so the counts are read once up to 65,536 pages (again for more), and
-// only the warps' totals meet across the block.
+// only the warps' totals meet across the block.  9 us on B200 for 10,500 pages (two rounds
+// of loads, three block scans); 16 loads in flight instead of 8 measured the same.
 constexpr int kPlanBits = 64;
 __global__ void __launch_bounds__(kBookThreads) mla_cache_compact_plan_kernel(const CacheBooks k, int32_t* ws) {
     __shared__ int tot[33];
@@ -818,6 +829,9 @@ __global__ void __launch_bounds__(kBookThreads) mla_cache_compact_plan_kernel(co
     }
 }
 
+// Moves the pages, then renames them in the tables of the rows in use.  7 CTAs per SM are
+// resident; 8, 16, 24 or 32 per SM in the grid: 52.8, 49.4, 48.3, 48.7 us for the books,
+// the plan and 182 MB of moves.
 __global__ void __launch_bounds__(kCopyThreads)
     mla_cache_compact_kernel(const CacheBooks k, const CachePool pool, const int32_t* ws, int shift) {
     griddep_wait();  // the plan

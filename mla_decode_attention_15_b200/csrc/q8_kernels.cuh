@@ -29,12 +29,26 @@
 // Work split.  A step is 128 tokens (two pages; M = 128 in GEMM1), cut into four
 // boxes of 128 latent columns (16 KB each, 128-byte swizzle) and the 64 RoPE
 // columns (8 KB).  Box c is both K columns [128 c, 128 c + 128) of GEMM1 and the
-// d_v chunk c of GEMM2 (read MN-major), so the ring that holds the boxes frees
-// each one as soon as its chunk's GEMM2 is done.  The plan, the walk over work
-// items, the partial slots and the combine are those of decode_kernels.cuh
-// (64-token units).  Query groups are 16 or 32 columns; more query columns are
-// several groups that walk each range of pages side by side, one CTA per group,
-// so that all but the first read of a page hit L2.
+// d_v chunk c of GEMM2 (read MN-major).  The ring holds them two boxes to a slot,
+// and GEMM2 frees a slot as soon as both of its chunks are done.  The plan, the
+// walk over work items, the partial slots and the combine are those of
+// decode_kernels.cuh (64-token units, with an overhead per item of their own).
+// Query groups are 16 or 32 columns; more query columns are several groups that
+// walk each range of pages side by side, one CTA per group, so that all but the
+// first read of a page hit L2.
+//
+// What bounds it, on B200 (event-timed, caches warm):
+//   - 16 requests x 64K x 16 heads, 605 MB: 121 us, 5.0 TB/s of the 6.55 TB/s of a
+//     plain copy.  A steady step keeps up with the loads; the rest is the first
+//     items' Q split and last items' epilogue, the combine (7 us by itself), and the
+//     clock, which the power limit lowers in a long run.
+//   - 32 requests x 8-32K x 2 tokens x 128 heads, 365 GFLOP on 395 MB: 555 us, 0.66 PFLOP/s of
+//     the sums as defined (0.40 of the measured bf16 rate).  A step's
+//     tensor work (two Q terms, three P terms of 32 columns) is 1,760 cycles; its softmax,
+//     a chain of TMEM read, exponentials, three conversions and the store of P^T,
+//     about 2,950.
+//   - 16 requests x 1-16K x 2 tokens x 16 heads, 81 MB: 39 us; 1 x 1K: 11.4 us.  An item's
+//     fixed parts: plan, Q split, first step, epilogue, combine.
 #pragma once
 
 #include <cuda_bf16.h>
