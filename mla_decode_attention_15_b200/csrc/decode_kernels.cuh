@@ -636,7 +636,10 @@ __device__ void run_producer(const CUtensorMap* kv_map, const CUtensorMap* q_map
                     prefetch_l2_bulk(p.kv + (size_t)ph * L::kStageBytes, L::kStageBytes);
             }
             const int st = kv_it % L::kStages;
-            ok = wait_bounded(bar0 + 8 * (kKvEmpty0 + st), ((kv_it / L::kStages) & 1) ^ 1, ctl);
+            // The first page, issued before, may already have been used and its stage
+            // freed while this thread issued Q: a wait for the phase before that would
+            // never end.
+            ok = first_page_issued || wait_bounded(bar0 + 8 * (kKvEmpty0 + st), ((kv_it / L::kStages) & 1) ^ 1, ctl);
             if (!ok) break;
             if (stall) {  // test hook: this page is never loaded, so its GEMM1 wait runs out
                 stall = false;
