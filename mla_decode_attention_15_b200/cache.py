@@ -141,6 +141,17 @@ def _launch_stream(device: torch.device, stream) -> int:
     return int(stream)
 
 
+def _empty(shape, dtype, device, stream, what: str) -> torch.Tensor:
+    """Memory for a launch on ``stream``, from that stream's pool: the current
+    stream's may still be in use by work that is queued there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        _fail("a raw stream handle needs %s of the caller's", what)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _status(status: Optional[torch.Tensor], device) -> Optional[int]:
     if status is None:
         return None
@@ -182,14 +193,14 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, rope: mla_rope_table, o
     rotated for positions [T] (int32); the other columns pass through.  Rows
     may be strided (multiples of 8 values); ``out=x`` rotates in place.
     ``transpose`` applies the transposed map: the gradient of x from that of
-    the result."""
+    the result.  Without ``out`` the result belongs to ``stream`` (a torch.cuda.Stream)."""
     shape, dtype, device = x.shape, x.dtype, x.device
     if len(shape) not in (2, 3):
         _fail("x must be [T, h, W] or [T, W]")
     if dtype is not _BF16 and dtype is not _F32:
         _fail("x must be bf16 or fp32")
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
+        out = _empty(shape, dtype, device, stream, "out")
     elif out.shape != shape or out.dtype is not dtype or out.device != device:
         _fail("out must have the shape, type and device of x")
     T, W = shape[0], shape[-1]
@@ -328,11 +339,7 @@ def cache_copy_pages(src: torch.Tensor, dst: torch.Tensor, kv_cache: torch.Tenso
 
 def _workspace(workspace, need: int, device, stream) -> torch.Tensor:
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:  # it is dropped before the stream has run
-            if not isinstance(stream, torch.cuda.Stream):
-                _fail("a raw stream handle needs a workspace of the caller's")
-            workspace.record_stream(stream)
+        workspace = _empty(need, torch.uint8, device, stream, "a workspace")
     elif workspace.dtype is not torch.uint8 or workspace.numel() < need or not workspace.is_contiguous() or \
             workspace.device != device:
         _fail("workspace must be %d bytes (uint8) on %s", need, device)
@@ -438,7 +445,8 @@ class Q8Decoder:
         _i32(cache_seqlens, self._bt_shape[:1], "cache_seqlens", device)
 
     def plan(self, cache_seqlens: torch.Tensor, stream=None) -> None:
-        mla_decode_q8_get_schedule(self.dims, cache_seqlens, self.schedule, stream)
+        _i32(cache_seqlens, self._bt_shape[:1], "cache_seqlens", self.out.device)
+        mla_decode_q8_get_schedule(self.dims, cache_seqlens, self.schedule, _launch_stream(self.out.device, stream))
 
     def __call__(self, q, kv_cache, kv_scales, block_table, cache_seqlens, softmax_scale: float, stream=None,
                  check: bool = True) -> Tuple[torch.Tensor, torch.Tensor]:

@@ -520,3 +520,14 @@ def test_absorbed_step_is_its_parts(dev, s_q, h, inline, q8):
     pool = wide(dict(kv=pools[1][0].cpu(), scales=pools[1][1].cpu())) if q8 else pools[1][0].cpu()
     ref, rl = oracle.mla_oracle_fwd(d["q"], pool, d["bt"], d["lens"], SCALE, causal=s_q > 1)
     helpers.compare(o, lse, ref, rl)
+
+
+def test_plan_checks_the_lengths(dev):
+    dec = ca.Q8Decoder(4, 1, 16, 8, 2, device=dev)
+    ok = torch.ones(4, dtype=torch.int32, device=dev)
+    dec.plan(ok)
+    for bad in (ok[:3], ok.long(), ok.cpu(), torch.ones(8, dtype=torch.int32, device=dev)[::2]):
+        with pytest.raises(ValueError):
+            dec.plan(bad)
+    torch.cuda.synchronize()
+    assert dec.status() == 0

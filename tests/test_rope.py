@@ -143,3 +143,25 @@ def test_rope_stream_and_graph(dev):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, ca.rope_apply(x, pos, table, offset=128))
+
+
+def test_result_of_another_stream_is_not_shared(dev):
+    """Memory freed on the current stream, with work on it still queued, is not the result of a
+    call on another stream."""
+    table = ca.make_rope()
+    x, pos = _rand((64, 16, 192), torch.bfloat16, 6).to(dev), torch.arange(64, dtype=torch.int32, device=dev)
+    ref = ca.rope_apply(x, pos, table, offset=128)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    old = torch.empty_like(x)
+    torch.cuda._sleep(20_000_000)
+    old.fill_(7.0)
+    del old
+    got = ca.rope_apply(x, pos, table, offset=128, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(got, ref)
+    with pytest.raises(ValueError):
+        ca.rope_apply(x, pos, table, offset=128, stream=s.cuda_stream)
+    ca.rope_apply(x, pos, table, offset=128, out=got, stream=s.cuda_stream)
+    s.synchronize()
+    assert torch.equal(got, ref)
