@@ -159,7 +159,9 @@ int mla_cache_append(const mla_cache_dims* dims, int32_t tokens, const void* c_k
 /* For i < n (1 .. 1024): row children[i], which must be empty, becomes a copy
  * of row parents[i]: it shares the parent's full pages (their counts rise), and
  * a last page that is not full is copied (with its scale) into the lowest free
- * page, in the order of i, so that both rows may be written on.  A fork that
+ * page, in the order of i, so that both rows may be written on.  Parents are
+ * taken as they are before the call: one that is a child of the same call is empty
+ * then, and so is its child.  A fork that
  * cannot be made (MLA_STATUS_BAD_ROW; _NO_FREE_PAGE; _BAD_BLOCK_TABLE for its
  * last page) leaves its child empty; a bad entry among the full pages is copied
  * as it is, with that word.  parents and children are device int32 [n], 4-byte

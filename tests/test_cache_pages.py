@@ -99,6 +99,13 @@ def test_fork_of_many_rows_and_of_forks(dev):
     w.check()
 
 
+def test_fork_takes_parents_as_they_were(dev):
+    w = World([200, 64], 40, dev, rows=6, seed=9)
+    w.fork([0, 2, 1, 2], [2, 3, 4, 5])
+    w.check()
+    assert w.lens.tolist() == [200, 64, 200, 0, 64, 0]
+
+
 def test_fork_refusals(dev):
     """Rows outside the batch, a child in use, a child named twice, itself: left out. The rest goes on."""
     w = World([100, 200, 30], 40, dev, rows=8, seed=6)
