@@ -202,8 +202,9 @@ def prepare(case, seed):
             _quantise(x, part, sc)
         s["bt"], s["lens"] = bt.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
         if own:  # the decoder a program keeps for a shape of batch: plan and workspace buffers
-            s["decoder"] = _ops().Q8Decoder(case["batch"], case["s_q"], case["heads"], num_blocks, bt.shape[1],
-                                            causal=case["s_q"] > 1, device=torch.device("cuda"), inline_plan=True)
+            from mla_decode_attention_15_b200 import Q8Decoder
+            s["decoder"] = Q8Decoder(case["batch"], case["s_q"], case["heads"], num_blocks, bt.shape[1],
+                                     causal=case["s_q"] > 1, device=torch.device("cuda"), inline_plan=True)
             s["decoder"].plan(s["lens"])
     elif op == "fork":
         lens = _spread(case["lo"], case["hi"], case["parents"])
@@ -250,25 +251,6 @@ def _rope_config(layout, scaling):
     return dict(YARN if scaling == "yarn" else PLAIN_ROPE, interleaved=layout == "interleaved")
 
 
-_loaded = None
-
-
-def _ops():
-    """The framework, loaded once as a program does."""
-    global _loaded
-    if _loaded is None:
-        import mla_decode_attention_15_b200
-        _loaded = mla_decode_attention_15_b200
-    return _loaded
-
-
-def _own_rope(s):
-    """The rotary table a program keeps for its model."""
-    if "rope" not in s:
-        s["rope"] = _ops().make_rope(**_rope_config(s["layout"], s["scaling"]))
-    return s["rope"]
-
-
 def run(s):
     return {"rope": _rope, "append": _append, "attend": _attend, "fork": _fork, "compact": _compact}[s["op"]](s)
 
@@ -301,9 +283,12 @@ def _rotate(x, positions, cfg, transpose=False):
 
 
 def _rope(s):
-    if own:
-        return _ops().rope_apply(s["x"], s["positions"], _own_rope(s), offset=ROPE_AT, out=s["out"], transpose=s["transpose"])
     cfg = _rope_config(s["layout"], s["scaling"])
+    if own:
+        from mla_decode_attention_15_b200 import make_rope, rope_apply
+        if "rope" not in s:
+            s["rope"] = make_rope(**cfg)
+        return rope_apply(s["x"], s["positions"], s["rope"], offset=ROPE_AT, out=s["out"], transpose=s["transpose"])
     y = s["out"]
     y.copy_(s["x"])
     y[..., ROPE_AT:] = _rotate(s["x"][..., ROPE_AT:], s["positions"], cfg, s["transpose"]).to(y.dtype)
@@ -311,11 +296,14 @@ def _rope(s):
 
 
 def _append(s):
+    cfg = _rope_config(s["layout"], s["scaling"])
     kv, scales = s["kv"], s["scales"]
     if own:
-        _ops().cache_append(s["c_kv"], s["k_pe"], s["off"], s["bt"], s["lens"], kv, scales, rope=_own_rope(s))
+        from mla_decode_attention_15_b200 import cache_append, make_rope
+        if "rope" not in s:
+            s["rope"] = make_rope(**cfg)
+        cache_append(s["c_kv"], s["k_pe"], s["off"], s["bt"], s["lens"], kv, scales, rope=s["rope"])
         return (kv, scales) if scales is not None else kv
-    cfg = _rope_config(s["layout"], s["scaling"])
     lens, off, bt = s["lens"].long(), s["off"].long(), s["bt"].long()
     n = off[1:] - off[:-1]
     start = lens - n
@@ -385,11 +373,11 @@ def _state(s):
 
 def _fork(s):
     bt, lens, refs = _reset(s)
-    kv, scales = s["kv"], s["scales"]
+    kv, scales, src, dst = s["kv"], s["scales"], s["src"].long(), s["dst"].long()
     if own:
-        _ops().cache_fork(s["src"], s["dst"], bt, lens, refs, kv, scales)
+        from mla_decode_attention_15_b200 import cache_fork
+        cache_fork(s["src"], s["dst"], bt, lens, refs, kv, scales)
         return _state(s)
-    src, dst = s["src"].long(), s["dst"].long()
     L = lens[src].long()
     part, last = L % PAGE > 0, L // PAGE
     # the k-th fork that ends inside a page takes the k-th free page
@@ -417,15 +405,15 @@ def _fork(s):
 
 def _compact(s):
     bt, lens, refs = _reset(s)
-    kv, scales = s["kv"], s["scales"]
+    kv, scales, rows = s["kv"], s["scales"], s["rows"].long()
     if own:
-        ops = _ops()
-        ops.cache_free(s["rows"], bt, lens, refs)
+        from mla_decode_attention_15_b200 import cache_compact, cache_free
+        cache_free(s["rows"], bt, lens, refs)
         if "compact_space" not in s:
-            s["compact_space"] = ops.cache_compact_workspace(kv.shape[0], kv.device)
-        ops.cache_compact(bt, lens, refs, kv, scales, workspace=s["compact_space"])
+            from mla_decode_attention_15_b200 import cache_compact_workspace
+            s["compact_space"] = cache_compact_workspace(kv.shape[0], kv.device)
+        cache_compact(bt, lens, refs, kv, scales, workspace=s["compact_space"])
         return _state(s)
-    rows = s["rows"].long()
     place = torch.arange(bt.shape[1], device="cuda")[None]
     used = place < -(-lens[:, None] // PAGE)
     gone = used[rows]
