@@ -206,7 +206,9 @@ int mla_cache_compact(const mla_cache_dims* dims, int32_t* block_table, const in
  *
  * The cache's bytes are multiplied as they are; neither the query nor the
  * softmax weights are rounded to 8 bits: a query value is within 2^-21 of its
- * row's largest magnitude, a weight within 2^-12 of itself or 2^-22 of the largest.
+ * row's largest magnitude (rows whose largest is 2^-92 or more), and a weight is
+ * held in 11 bits, within 2^-12 of itself, or its product with its page's scale is
+ * within 2^-22 of the row's largest such product.  That holds for fp32 results too.
  * Rows past a request's length, and its last page's unused rows, may hold
  * anything.  A NaN in a row that one query token sees reaches every query token
  * of its request.

@@ -17,14 +17,18 @@
 //     hi = e4m3(x) leaves a remainder of at most 4 significant bits, which
 //     lo = e4m3(16 (x - hi)) holds exactly.  Only values below 2^-14 of the
 //     row's largest are rounded, by at most 2^-21 of it.  S^T = S_hi + S_lo / 16.
-//   - P.  x = 16 p s / R (s the page's scale, R the largest scale so far) is rounded
-//     to fp16 (11 bits, half a step is 2^-12 of the weight: an eighth of the
-//     rounding of a bf16 result) and cut into three e4m3 terms, each 16 times the
-//     remainder of the one before, which hold those 11 bits exactly; values below
-//     2^-6 lose at most 2^-18 absolutely, 2^-22 of the largest weight.
-//     O^T = (O_0 + O_1 / 16 + O_2 / 256) R / 16.
+//   - P.  x = 16 p s / (the largest p s of the query column so far; s the page's
+//     scale) is rounded to fp16 (11 bits, half a step is 2^-12 of the weight: an
+//     eighth of the rounding of a bf16 result) and cut into three e4m3 terms, each
+//     16 times the remainder of the one before, which hold those 11 bits exactly;
+//     values below 2^-6 lose at most 2^-18 absolutely, 2^-22 of the largest.
+//     O^T = O_0 + O_1 / 16 + O_2 / 256.
 // The page's scale s is a factor of the score of its tokens and of their value
-// rows, so it enters the exponent of P and costs no pass over the data.
+// rows, so it enters the exponent of P and costs no pass over the data.  The running
+// reference m of a column is that of the sum w = z log2 e + log2 s, which is what is stored: a page
+// whose scale is large but whose tokens have no weight moves nothing.  The
+// sum of the weights, of x / s, stands against the same reference, so
+// out = O / l, and whatever w is rounded by, numerator and sum share it.
 //
 // Work split.  A step is 128 tokens (two pages; M = 128 in GEMM1), cut into four
 // boxes of 128 latent columns (16 KB each, 128-byte swizzle) and the 64 RoPE
@@ -76,7 +80,9 @@ constexpr float kQ8Bias = 4.0f;
 constexpr float kQ8Grow = 4.8f;
 // The Q warps wait for most of an item; they leave the issue slots alone meanwhile.
 constexpr int kQ8Nap = 200, kQ8MaxNaps = 1 << 22;  // ns; about a second
-constexpr float kQ8MinBias = -60.0f;
+// Where a page's scale is below this share of the largest so far, its tokens may carry all
+// the weight and yet x may vanish: their part of the sum is then computed without x.
+constexpr float kQ8FarScale = 0x1p-60f;
 constexpr float kQ8Unset = -3.402823466e38f;    // running max before the first visible token: below every score
 
 struct Q8Params : FwdParams {
@@ -601,13 +607,19 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             m[c] = kQ8Unset;
             l[c] = 0.f;
         }
-        float R = fmaxf(sc0, sc1);
-        float bias = 0.f, back = 0.f, bias_ks = -1.f, bias_R = -1.f;
+        float R = 0.f;  // the largest scale so far
+        float lks = 0.f, back = 0.f, of_ks = -1.f;
         for (int j = item.p0; j < item.p1; j += 2) {
             const float nx0 = page_scale(ph0), nx1 = page_scale(ph1);
             ph0 = entry(j + 4);
             ph1 = entry(j + 5);
             const float ks = wq < 2 ? sc0 : sc1;  // this token's page
+            R = fmaxf(R, fmaxf(sc0, sc1));
+            if (ks != of_ks) {  // (page scales seldom differ)
+                of_ks = ks;
+                lks = log2f(ks);
+                back = 1.f / ks;  // x -> its part of the sum
+            }
             const int sb = s_it & 1;
             ok = wait_warp(bar0 + 8 * (kQbSFull0 + sb), (s_it >> 1) & 1, ctl);
             if (!ok) break;
@@ -624,10 +636,10 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
 #pragma unroll
                 for (int c4 = 0; c4 < W / 4; ++c4) {
                     const float4 f = qs4[c4];
-                    z[4 * c4 + 0] = fmaf(lo[4 * c4 + 0], 0.0625f, z[4 * c4 + 0]) * (f.x * ks);
-                    z[4 * c4 + 1] = fmaf(lo[4 * c4 + 1], 0.0625f, z[4 * c4 + 1]) * (f.y * ks);
-                    z[4 * c4 + 2] = fmaf(lo[4 * c4 + 2], 0.0625f, z[4 * c4 + 2]) * (f.z * ks);
-                    z[4 * c4 + 3] = fmaf(lo[4 * c4 + 3], 0.0625f, z[4 * c4 + 3]) * (f.w * ks);
+                    z[4 * c4 + 0] = fmaf(fmaf(lo[4 * c4 + 0], 0.0625f, z[4 * c4 + 0]), f.x * ks, lks);
+                    z[4 * c4 + 1] = fmaf(fmaf(lo[4 * c4 + 1], 0.0625f, z[4 * c4 + 1]), f.y * ks, lks);
+                    z[4 * c4 + 2] = fmaf(fmaf(lo[4 * c4 + 2], 0.0625f, z[4 * c4 + 2]), f.z * ks, lks);
+                    z[4 * c4 + 3] = fmaf(fmaf(lo[4 * c4 + 3], 0.0625f, z[4 * c4 + 3]), f.w * ks, lks);
                 }
             }
             const int t = j * kPage + row;
@@ -642,7 +654,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                     if (t >= lim || t >= end) z[c] = -INFINITY;
                 }
             }
-            // Does any weight exceed the running reference by more than 2^kQ8Grow?
+            // Does any x exceed the running reference by more than 2^kQ8Grow?
             // The first step, which sets the reference, exchanges its maxima at once.
             const bool first = j == item.p0;
             const uint32_t vbar = bar0 + 8 * (kQbVote0 + (s_it & 1) * 2 + cg);
@@ -662,35 +674,34 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             arrive(vbar);
             ok = wait_warp(vbar, (s_it >> 1) & 1, ctl);
             if (!ok) break;
-            const float Rn = fmaxf(R, fmaxf(sc0, sc1));
             bool grown = first;
             if (!first) {
                 const uint4 v4 = *reinterpret_cast<const uint4*>(vote + (s_it & 1) * 8);
                 grown = (v4.x | v4.y | v4.z | v4.w) != 0;  // the same for the group's four warps
             }
-            if (grown || Rn > R) {
+            if (grown) {
                 // Move the references and rescale what is accumulated.
-                if (grown && !first) {
+                if (!first) {
                     post_maxima();
                     arrive(bar0 + 8 * (kQbMax0 + cg));
                     ok = wait_warp(bar0 + 8 * (kQbMax0 + cg), max_it & 1, ctl);
                     ++max_it;
                     if (!ok) break;
                 }
-                const float ra = R / Rn;
                 float alpha[W];
 #pragma unroll
                 for (int c = 0; c < W; ++c) {
-                    // (without branches: a column that stays has a = 2^0)
+                    // (without branches: a column that stays has a = 2^0.  A reference may
+                    // move further than fp32's exponents reach while the sum, whose
+                    // unit is 1 / scale, still counts: its factor is applied in two halves)
                     const float4 r4 = *reinterpret_cast<const float4*>(red + c * 4);
                     const float mx = fmaxf(fmaxf(r4.x, r4.y), fmaxf(r4.z, r4.w));
-                    const float to = grown && mx > m[c] + kQ8Grow ? mx : m[c];
-                    const float a = ex2_approx(m[c] - to);
+                    const float to = mx > m[c] + kQ8Grow ? mx : m[c];
+                    const float a = ex2_approx(0.5f * (m[c] - to));
                     m[c] = to;
-                    l[c] *= a;
-                    alpha[c] = a * ra;
+                    l[c] = l[c] * a * a;
+                    alpha[c] = a * a;
                 }
-                R = Rn;
                 if (j > item.p0) {
                     const uint32_t prev = s_it - 1;
                     ok = wait_warp(bar0 + 8 * (kQbPEmpty0 + prev % C::kPBufs), (prev / C::kPBufs) & 1, ctl);
@@ -714,27 +725,18 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                     tmem_st_wait();
                 }
             }
-            if (ks != bias_ks || R != bias_R) {  // (page scales seldom differ, and the largest seldom grows)
-                bias_ks = ks;
-                bias_R = R;
-                bias = kQ8Bias + __log2f(ks / R);
-                back = exp2f(-bias);  // x -> p
-            }
-            if (bias > kQ8MinBias) {
+            if (ks >= R * kQ8FarScale) {
 #pragma unroll
                 for (int c = 0; c < W; ++c) {
-                    z[c] = ex2_approx(z[c] - m[c] + bias);
+                    z[c] = ex2_approx(z[c] - m[c] + kQ8Bias);
                     l[c] = fmaf(z[c], back, l[c]);
                 }
             } else {
-                // A page whose values are next to nothing beside the largest
-                // page's still counts in full in the sum of the weights.
-                const float f = exp2f(bias);
 #pragma unroll
                 for (int c = 0; c < W; ++c) {
-                    z[c] = ex2_approx(z[c] - m[c]);
-                    l[c] += z[c];
-                    z[c] *= f;
+                    const float w = z[c] - m[c] + kQ8Bias;
+                    l[c] += ex2_approx(w - lks);
+                    z[c] = ex2_approx(w);
                 }
             }
             const uint32_t pb = s_it % C::kPBufs;
@@ -784,13 +786,17 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
         for (int c = 0; c < W; ++c) {
             const float4 s4 = *reinterpret_cast<const float4*>(sums + c * 4);
             const float ls = (s4.x + s4.y) + (s4.z + s4.w);
-            inv[c] = ls == 0.f ? 0.f : R * 0.0625f * rcp_approx(ls);
+            inv[c] = ls == 0.f ? 0.f : rcp_approx(ls);
             m_own = row == c ? m[c] : m_own;
             l_own = row == c ? ls : l_own;
         }
         if (row < W && gc0 + row < p.N) {
             const int gc = gc0 + row;
-            const float lse = l_own == 0.f ? -INFINITY : (m_own + log2f(l_own)) * kLn2;
+            // (the exponents are added first: the sum's unit is a scale's inverse, and what is
+            // left of large ones is small)
+            int e;
+            const float part = log2f(frexpf(l_own, &e));
+            const float lse = l_own == 0.f ? -INFINITY : ((m_own + ((float)e - kQ8Bias)) + part) * kLn2;
             if (item.unsplit) {
                 const int sq = gc >= p.heads ? 1 : 0;  // (at most two query tokens)
                 p.lse[((size_t)item.b * p.heads + (gc - sq * p.heads)) * p.s_q + sq] = lse;

@@ -531,3 +531,91 @@ def test_plan_checks_the_lengths(dev):
             dec.plan(bad)
     torch.cuda.synchronize()
     assert dec.status() == 0
+
+
+# ------------------------------------------------------------------ scales far apart
+def exact(d, scale=SCALE, causal=False):
+    """fp64 attention over the cache's own values, any scales: (out [rows, 512], lse [rows], a bound on an
+    fp32 output, a bound on lse).  Per token t with weight w_t, page scale s_t and score error e_t:
+      - its weight is rounded by 2^-12 of itself, or its product with s_t is cut off below 2^-22 of the largest
+        product w s of the row; a value is at most 448 s
+      - exponentials, sums, merge of splits and the division in fp32:  2^-18 M
+      - e_t moves the row by e_t w_t (|v_t| + |out|): fp32 sums of the products, the query's remainder,
+        and z + log2 s, its difference to the reference and the base's 4, each rounded in fp32 (in
+        units of log2: 2^-24 of at most 2 (|z| + |log2 s|) + 4, four times)"""
+    B, s_q, h, _ = d["q"].shape
+    out, tol = torch.zeros(B, s_q, h, 512, dtype=torch.float64), torch.zeros(B, s_q, h, 512, dtype=torch.float64)
+    lse, ltol = torch.full((B, s_q, h), -float("inf"), dtype=torch.float64), torch.zeros(B, s_q, h, dtype=torch.float64)
+    for b in range(B):
+        L = int(d["lens"][b])
+        ids = d["bt"][b, :(L + 63) // 64].long()
+        s = d["scales"][ids].double().repeat_interleave(64, 0)[:L, 0]
+        k = d["kv"][ids].double().reshape(-1, 576)[:L] * s[:, None]
+        for i in range(s_q):
+            n = L - s_q + 1 + i if causal and s_q > 1 else L
+            if n <= 0:
+                continue
+            q, kk, v = d["q"][b, i].double(), k[:n], k[:n, :512].abs()
+            z = q @ kk.T * scale
+            w = torch.softmax(z, -1)
+            lse[b, i], out[b, i] = torch.logsumexp(z, -1), w @ kk[:, :512]
+            e = abs(scale) * (1152 * 2.0 ** -24 * (q.abs() @ kk.abs().T) + 2.0 ** -21 * q.abs().amax(-1)[:, None] * kk.abs().sum(-1))
+            e = e + 2.0 ** -21 * (z.abs() * 1.5 + torch.log2(s[:n]).abs() + 4)
+            we = w * e
+            tol[b, i] = ((2.0 ** -12 + 2.0 ** -18) * w + we) @ v + we.sum(-1)[:, None] * out[b, i].abs() + \
+                (2.0 ** -22 * n * 448 * (w * s[:n]).amax(-1))[:, None] + 2.0 ** -148
+            ltol[b, i] = we.sum(-1) + 2.0 ** -20 + 2.0 ** -21 * lse[b, i].abs()
+    return out, lse, tol, ltol
+
+
+def check64(d, out, lse, scale=SCALE, causal=False):
+    ref, rl, tol, ltol = exact(d, scale, causal)
+    err = (out.double() - ref).abs()
+    assert bool((err <= tol).all()), (float((err / tol).max()), (~(err <= tol)).nonzero()[0].tolist())
+    got = lse.double().transpose(1, 2)
+    assert bool(((got == rl) | ((got - rl).abs() <= ltol)).all())
+
+
+def far_page(d, pages, scale):
+    """These pages (of the pool) get a scale, large latent values where no query looks, and a last
+    column that brings their scores far below the others'."""
+    d["q"][..., :32] = 0
+    d["q"][..., 575] = 4
+    g = torch.Generator().manual_seed(99)
+    for p in pages:
+        v = torch.zeros(64, 1, 576)
+        v[..., :32] = torch.randint(-448, 449, (64, 1, 32), generator=g)
+        v[..., 575] = -448
+        d["kv"][p], d["scales"][p] = v.to(torch.float8_e4m3fn), scale
+
+
+@pytest.mark.parametrize("h", [16, 32])
+@pytest.mark.parametrize("where", [[0], [5], [3, 8]])
+@pytest.mark.parametrize("k", [8, 14, 20, 30, 90])
+def test_a_page_of_a_large_scale_without_weight(dev, h, where, k):
+    """It takes nothing from the weights of the others, wherever it lies."""
+    d = build([1000, 700], 1, h, seed=50 + k)
+    far_page(d, [int(d["bt"][b, j]) for b in range(2) for j in where], 2.0 ** k)
+    for sms in (1, 3):
+        out, lse = run(d, dev, False, True, sms, fp32=True)
+        check64(d, out, lse)
+
+
+@pytest.mark.parametrize("h", [16, 32])
+@pytest.mark.parametrize("low", [-60, -100, -110])
+@pytest.mark.parametrize("first", [True, False])
+def test_weight_on_pages_of_a_small_scale(dev, h, low, first):
+    """Nearly all the weight on pages far smaller than the rest, before, between and behind them: the
+    sum of the weights is theirs, whatever the others' values are worth."""
+    d = build([900], 1, h, seed=70)
+    ids = d["bt"][0].long()
+    small = ids[0::3] if first else ids[1::3]
+    d["q"][..., :575] *= 2.0 ** -4
+    d["q"][..., 575] = 16
+    d["kv"][ids, :, :, 575] = torch.tensor(-40.0).to(torch.float8_e4m3fn)  # -46 of score, and some 10 around it
+    d["kv"][small] = torch.randn(len(small), 64, 1, 576, generator=torch.Generator().manual_seed(3)).to(torch.float8_e4m3fn)
+    d["scales"][ids] = 1.0
+    d["scales"][small] = 2.0 ** low
+    for sms in (1, 2):
+        out, lse = run(d, dev, False, True, sms, fp32=True)
+        check64(d, out, lse)
