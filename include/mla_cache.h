@@ -198,7 +198,9 @@ int mla_cache_compact(const mla_cache_dims* dims, int32_t* block_table, const in
  * Decode attention over the 8-bit cache: the operation, the arguments, the
  * flags, the split-KV plan and the status word of mla_decode.h, with
  *   kv_cache   e4m3 [num_blocks][64][1][576]
- *   kv_scales  fp32 [num_blocks][1], positive and finite
+ *   kv_scales  fp32 [num_blocks][1], positive and finite; those of one request within
+ *              2^220 of each other (any that mla_cache_append writes are).  A scale that
+ *              is 0, negative or NaN is read as 2^-100
  * The schedule and workspace sizes come from the two _bytes calls below, and
  * the plan from these get_schedule calls (the query groups are 16 or 32
  * columns wide).  MLA_FLAG_INLINE_PLAN builds the plan in the decode kernel up

@@ -83,6 +83,10 @@ constexpr int kQ8Nap = 200, kQ8MaxNaps = 1 << 22;  // ns; about a second
 // Where a page's scale is below this share of the largest so far, its tokens may carry all
 // the weight and yet x may vanish: their part of the sum is then computed without x.
 constexpr float kQ8FarScale = 0x1p-60f;
+// A range's sum of weights is counted in 1 / scale, which fp32 holds (with 2^20 tokens) down
+// to scales of 2^-100; with a page below that in the range, in units of 2^50.
+constexpr float kQ8SmallScale = 0x1p-100f;
+constexpr int kQ8SmallUnit = -50;
 constexpr float kQ8Unset = -3.402823466e38f;    // running max before the first visible token: below every score
 
 struct Q8Params : FwdParams {
@@ -596,8 +600,9 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
         const int32_t* bt = p.block_table + (size_t)item.b * p.max_blocks;
         auto entry = [&](int j) { return __ldg(bt + (j < item.p1 ? j : item.p1 - 1)); };
         auto page_scale = [&](int phys) -> float {
-            // (a page of scale 0 holds zeros; the floor keeps its tokens' weights finite)
-            return fmaxf(__ldg(p.kv_scales + ((unsigned)phys < (unsigned)p.num_blocks ? phys : 0)), 1e-30f);
+            // (a scale of 0 goes with zeros: any other one keeps its tokens' weights finite)
+            const float s = __ldg(p.kv_scales + ((unsigned)phys < (unsigned)p.num_blocks ? phys : 0));
+            return s > 0.f ? s : kQ8SmallScale;
         };
         float sc0 = page_scale(entry(item.p0)), sc1 = page_scale(entry(item.p0 + 1));
         int ph0 = entry(item.p0 + 2), ph1 = entry(item.p0 + 3);
@@ -609,6 +614,8 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
         }
         float R = 0.f;  // the largest scale so far
         float lks = 0.f, back = 0.f, of_ks = -1.f;
+        float small = kQ8SmallScale;  // 0 once l counts in units of 2^kQ8SmallUnit
+        auto unit = [&]() { return small > 0.f ? 0 : kQ8SmallUnit; };
         for (int j = item.p0; j < item.p1; j += 2) {
             const float nx0 = page_scale(ph0), nx1 = page_scale(ph1);
             ph0 = entry(j + 4);
@@ -618,7 +625,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             if (ks != of_ks) {  // (page scales seldom differ)
                 of_ks = ks;
                 lks = log2f(ks);
-                back = 1.f / ks;  // x -> its part of the sum
+                back = (ks < small ? pow2f(kQ8SmallUnit) : pow2f(unit())) / ks;  // x -> its part of the sum
             }
             const int sb = s_it & 1;
             ok = wait_warp(bar0 + 8 * (kQbSFull0 + sb), (s_it >> 1) & 1, ctl);
@@ -665,7 +672,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             if (first) {
                 post_maxima();
             } else {
-                bool grow = false;
+                bool grow = ks < small;  // (the unit of the sum changes as the references do)
 #pragma unroll
                 for (int c = 0; c < W; ++c) grow |= z[c] > m[c] + kQ8Grow;
                 const uint32_t gw = __any_sync(kFullMask, grow) ? 1u : 0u;
@@ -689,6 +696,12 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                     if (!ok) break;
                 }
                 float alpha[W];
+                float to_unit = 1.f;
+                if (fminf(sc0, sc1) < small) {
+                    to_unit = pow2f(kQ8SmallUnit);
+                    if (ks >= small) back *= to_unit;
+                    small = 0.f;
+                }
 #pragma unroll
                 for (int c = 0; c < W; ++c) {
                     // (without branches: a column that stays has a = 2^0.  A reference may
@@ -699,7 +712,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                     const float to = mx > m[c] + kQ8Grow ? mx : m[c];
                     const float a = ex2_approx(0.5f * (m[c] - to));
                     m[c] = to;
-                    l[c] = l[c] * a * a;
+                    l[c] = l[c] * a * a * to_unit;
                     alpha[c] = a * a;
                 }
                 if (j > item.p0) {
@@ -735,7 +748,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
 #pragma unroll
                 for (int c = 0; c < W; ++c) {
                     const float w = z[c] - m[c] + kQ8Bias;
-                    l[c] += ex2_approx(w - lks);
+                    l[c] += ex2_approx(w - lks + (float)unit());
                     z[c] = ex2_approx(w);
                 }
             }
@@ -796,7 +809,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             // left of large ones is small)
             int e;
             const float part = log2f(frexpf(l_own, &e));
-            const float lse = l_own == 0.f ? -INFINITY : ((m_own + ((float)e - kQ8Bias)) + part) * kLn2;
+            const float lse = l_own == 0.f ? -INFINITY : ((m_own + ((float)(e - unit()) - kQ8Bias)) + part) * kLn2;
             if (item.unsplit) {
                 const int sq = gc >= p.heads ? 1 : 0;  // (at most two query tokens)
                 p.lse[((size_t)item.b * p.heads + (gc - sq * p.heads)) * p.s_q + sq] = lse;
@@ -816,6 +829,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
         const size_t base = (item.unsplit ? (size_t)item.b * p.N + gc0 : (size_t)item.slot * NG + cg * W) * kDv + row;
         float* dst = (item.unsplit ? static_cast<float*>(p.out) : p.opart) + base;
         __nv_bfloat16* dst16 = static_cast<__nv_bfloat16*>(p.out) + base;
+        const float scale = pow2f(unit());
 #pragma unroll 1
         for (int ch = 0; ch < kQ8Boxes; ++ch) {
             float o[W], o1[W], o2[W];
@@ -825,7 +839,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             tmem_ld_cols(ta + 2 * NG, o2);
             tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < W; ++c) o[c] = fmaf(fmaf(o2[c], 0.0625f, o1[c]), 0.0625f, o[c]) * inv[c];
+            for (int c = 0; c < W; ++c) o[c] = fmaf(fmaf(o2[c], 0.0625f, o1[c]), 0.0625f, o[c]) * inv[c] * scale;
             if (f32) {
 #pragma unroll
                 for (int c = 0; c < W; ++c)

@@ -602,6 +602,21 @@ def test_a_page_of_a_large_scale_without_weight(dev, h, where, k):
 
 
 @pytest.mark.parametrize("h", [16, 32])
+@pytest.mark.parametrize("e", [-140, -120, -101, -100, -98, -40, 60, 100, 119])
+def test_scales_of_any_size(dev, h, e):
+    """One or two scales for all pages, with queries that bring the scores back to size (up to
+    2^60; beside larger scales they are 0: every token weighs the same)."""
+    d = build([300, 65, 1], 1, h, seed=60)
+    g = torch.Generator().manual_seed(61)
+    d["scales"] = torch.exp2(torch.randint(0, 2, d["scales"].shape, generator=g).double() + e).float()
+    d["kv"] = (torch.randn(d["kv"].shape, generator=g) * 32).to(torch.float8_e4m3fn)
+    d["q"] = (d["q"].double() * (2.0 ** min(-5 - e, 120) if e <= 60 else 0.0)).bfloat16()
+    for sms in (1, 2):
+        out, lse = run(d, dev, False, True, sms, fp32=True)
+        check64(d, out, lse)
+
+
+@pytest.mark.parametrize("h", [16, 32])
 @pytest.mark.parametrize("low", [-60, -100, -110])
 @pytest.mark.parametrize("first", [True, False])
 def test_weight_on_pages_of_a_small_scale(dev, h, low, first):
