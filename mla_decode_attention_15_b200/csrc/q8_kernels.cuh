@@ -662,6 +662,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                 }
             }
             // Does any x exceed the running reference by more than 2^kQ8Grow?
+            // (The difference of two close numbers is exact; the sum of a large one and 4.8 is not.)
             // The first step, which sets the reference, exchanges its maxima at once.
             const bool first = j == item.p0;
             const uint32_t vbar = bar0 + 8 * (kQbVote0 + (s_it & 1) * 2 + cg);
@@ -674,7 +675,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
             } else {
                 bool grow = ks < small;  // (the unit of the sum changes as the references do)
 #pragma unroll
-                for (int c = 0; c < W; ++c) grow |= z[c] > m[c] + kQ8Grow;
+                for (int c = 0; c < W; ++c) grow |= z[c] - m[c] > kQ8Grow;
                 const uint32_t gw = __any_sync(kFullMask, grow) ? 1u : 0u;
                 if (lane == 0) vote[(s_it & 1) * 8 + wq] = gw;
             }
@@ -709,7 +710,7 @@ __device__ void q8_softmax(const Q8Params& p, const int32_t* meta, uint8_t* smem
                     // unit is 1 / scale, still counts: its factor is applied in two halves)
                     const float4 r4 = *reinterpret_cast<const float4*>(red + c * 4);
                     const float mx = fmaxf(fmaxf(r4.x, r4.y), fmaxf(r4.z, r4.w));
-                    const float to = mx > m[c] + kQ8Grow ? mx : m[c];
+                    const float to = mx - m[c] > kQ8Grow ? mx : m[c];
                     const float a = ex2_approx(0.5f * (m[c] - to));
                     m[c] = to;
                     l[c] = l[c] * a * a * to_unit;

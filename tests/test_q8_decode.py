@@ -634,3 +634,34 @@ def test_weight_on_pages_of_a_small_scale(dev, h, low, first):
     for sms in (1, 2):
         out, lse = run(d, dev, False, True, sms, fp32=True)
         check64(d, out, lse)
+
+
+@pytest.mark.parametrize("h", [16, 32])
+@pytest.mark.parametrize("exponent,rise,q", [(20, 5, 1), (22, 5, 1), (23, 5, 1), (24, 6, 2), (26, 8, 8), (27, 16, 8)])
+def test_large_scores_that_rise_a_little(dev, h, exponent, rise, q):
+    """Scores of a size at which fp32 has no room for a reference and a margin in one number.  Each is
+    exact: softmax_scale is ln 2, so scores are in units of log2, and q k = 2^exponent + rise i."""
+    n = 4
+    d = build([128 * n], 1, h, seed=80)
+    d["q"] = torch.zeros(d["q"].shape, dtype=torch.bfloat16)
+    d["q"][..., 574], d["q"][..., 575] = 2.0 ** (exponent - 8), q
+    kv = torch.randn(d["kv"].shape, generator=torch.Generator().manual_seed(4)) * 8
+    kv[..., 512:] = 0
+    kv[..., 574] = 128  # half of the score of the tokens that rise
+    for i in range(n):
+        row = kv[int(d["bt"][0, 2 * i]), 7 * i, 0]
+        row[574], row[575] = 256, rise * i // q
+    d["kv"], d["scales"] = kv.to(torch.float8_e4m3fn), torch.ones_like(d["scales"])
+    k = d["kv"][d["bt"][0].long()].double().reshape(-1, 576)
+    z = d["q"][0, 0].double() @ k.T
+    assert sorted(z[0].tolist())[-n:] == [2.0 ** exponent + rise * i for i in range(n)]
+    w = torch.softmax(z * np.log(2), -1)
+    g = {x: y.to(dev) for x, y in d.items()}
+    dec = ca.Q8Decoder(1, 1, h, d["kv"].shape[0], d["bt"].shape[1], False, 1, dev, fp32_out=True, inline_plan=True)
+    dec.plan(g["lens"])
+    out, _ = dec(g["q"], g["kv"], g["scales"], g["bt"], g["lens"], float(np.log(2)))
+    torch.cuda.synchronize()
+    assert dec.status() == 0
+    err = (out[0, 0].cpu().double() - w @ k[:, :512]).abs()
+    tol = (2.0 ** -12 + 2.0 ** -18) * (w @ k[:, :512].abs()) + 2.0 ** -22 * len(k) * 448 * w.amax(-1)[:, None]
+    assert bool((err <= tol).all()), float((err / tol).max())
