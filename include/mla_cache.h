@@ -130,7 +130,8 @@ int mla_rope_apply(const mla_rope_dims* dims, const mla_rope_table* table, const
  * keeps that so).  A request whose new rows do not fit (n_b < 0, n_b >
  * cache_seqlens[b], a length past max_blocks_per_seq pages, offsets past
  * tokens) is skipped whole with MLA_STATUS_BAD_ROW, rows of a page whose block-table
- * entry is outside the pool are skipped with MLA_STATUS_BAD_BLOCK_TABLE.
+ * entry is outside the pool are skipped with MLA_STATUS_BAD_BLOCK_TABLE; the other
+ * requests are written.
  * The kernel lets no dependent grid start before its writes are done, so a
  * decode call may follow it on the stream.
  * ---------------------------------------------------------------------- */

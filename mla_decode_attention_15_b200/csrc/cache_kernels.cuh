@@ -354,36 +354,13 @@ __device__ __forceinline__ uint32_t amax_of(uint32_t amax, float x) {
 constexpr int kAppendThreads = 512;
 constexpr int kLatRows = kPage * (kDv / 8) / kAppendThreads;  // 8
 static_assert(kPage * 8 == kAppendThreads, "one RoPE unit per thread");
+// Page `nth` of request b's new ones.
 template <bool kQ8>
-__global__ void __launch_bounds__(kAppendThreads, 2) mla_cache_append_kernel(const __grid_constant__ AppendParams p) {
-    __shared__ int tot[33];
-    __shared__ int job[4];  // request, page within its new pages
-    __shared__ uint32_t warp_max[kAppendThreads / 32];
+__device__ __forceinline__ void append_page(const AppendParams& p, int b, int nth, uint32_t* warp_max) {
     const int tid = threadIdx.x;
-    if (tid == 0) job[0] = -1;
-    int before = 0;
-    for (int base = 0; base < p.batch; base += kAppendThreads) {
-        const int b = base + tid;
-        bool bad = false;
-        int pages = 0;
-        if (b < p.batch) pages = new_rows(p, b, &bad).pages;
-        if (bad) raise(p.status, MLA_STATUS_BAD_ROW);
-        int total;
-        const int mine = before + block_exclusive(pages, tot, &total);
-        if ((int)blockIdx.x >= mine && (int)blockIdx.x < mine + pages) {
-            job[0] = b;
-            job[1] = blockIdx.x - mine;
-        }
-        before += total;
-        // (CTA 0 looks at every request, for the status)
-        if (blockIdx.x != 0 && (int)blockIdx.x < before) break;
-    }
-    __syncthreads();
-    const int b = job[0];
-    if (b < 0) return;
     bool bad = false;
     const NewRows nr = new_rows(p, b, &bad);
-    const int page = nr.start / kPage + job[1];
+    const int page = nr.start / kPage + nth;
     const int phys = p.bt[(size_t)b * p.max_blocks + page];
     if ((unsigned)phys >= (unsigned)p.pool.num_blocks) {
         if (tid == 0) raise(p.status, MLA_STATUS_BAD_BLOCK_TABLE);
@@ -533,11 +510,57 @@ __global__ void __launch_bounds__(kAppendThreads, 2) mla_cache_append_kernel(con
             }
         }
     }
+}
+
+// Finds page number `want` of all requests' new ones: job[0], job[1] = its request and place there (job[0]
+// stays -1: there is none), job[2] = the number of pages looked at, job[3] = want.  CTA 0 looks at every request, for the status.
+__device__ __forceinline__ void append_find(const AppendParams& p, int want, int* tot, int* job) {
+    const int tid = threadIdx.x;
+    if (tid == 0) job[0] = -1;
+    int before = 0;
+    for (int base = 0; base < p.batch; base += kAppendThreads) {
+        const int b = base + tid;
+        bool bad = false;
+        int pages = 0;
+        if (b < p.batch) pages = new_rows(p, b, &bad).pages;
+        if (bad) raise(p.status, MLA_STATUS_BAD_ROW);
+        int total;
+        const int mine = before + block_exclusive(pages, tot, &total);
+        if (want >= mine && want < mine + pages) {
+            job[0] = b;
+            job[1] = want - mine;
+        }
+        before += total;
+        if (blockIdx.x != 0 && want < before) break;
+    }
+    if (tid == 0) {
+        job[2] = before;
+        job[3] = want;
+    }
+    __syncthreads();
+}
+
+template <bool kQ8>
+__global__ void __launch_bounds__(kAppendThreads, 2) mla_cache_append_kernel(const __grid_constant__ AppendParams p) {
+    __shared__ int tot[33];
+    __shared__ int job[4];
+    __shared__ uint32_t warp_max[kAppendThreads / 32];
+    // Every page has a CTA while the offsets do not fall.  Where they do, requests that are in
+    // order may name the same rows, and more pages than there are CTAs: CTA 0 writes those one after the other.
+    for (int want = blockIdx.x;;) {
+        append_find(p, want, tot, job);
+        if (job[0] >= 0) append_page<kQ8>(p, job[0], job[1], warp_max);
+        if (blockIdx.x != 0) break;
+        want = max(job[3] + 1, (int)gridDim.x);
+        if (want >= job[2]) break;
+        __syncthreads();
+    }
     __threadfence();
 }
 
 inline void launch_append(const AppendParams& p, cudaStream_t stream) {
-    // n new rows touch at most n pages, and at most n / 64 + 2
+    // n new rows touch at most n pages, and at most n / 64 + 2; and the requests' rows are
+    // `tokens` in all, if their offsets do not fall
     const int64_t most = min((int64_t)p.tokens, (int64_t)p.tokens / kPage + 2 * (int64_t)p.batch);
     if (p.pool.scales != nullptr) mla_cache_append_kernel<true><<<(unsigned)most, kAppendThreads, 0, stream>>>(p);
     else mla_cache_append_kernel<false><<<(unsigned)most, kAppendThreads, 0, stream>>>(p);

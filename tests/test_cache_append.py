@@ -215,3 +215,24 @@ def test_append_stream_and_graph(dev):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(g["pool"].cpu().view(torch.uint8), ref.view(torch.uint8)) and torch.equal(g["scales"].cpu(), rs)
+
+
+@pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("B,T", [(3, 2000), (4, 190), (601, 64)])
+def test_append_with_falling_offsets(dev, B, T, q8):
+    """Offsets 0, T, 0, T, ...: every second request is refused, and the others, which name the same rows, are
+    written whole, although together they have more pages than T rows of requests in order."""
+    d = _make([70] * B, [T] + [0] * (B - 1), q8, seed=B)
+    good = list(range(0, B, 2))
+    pages = oc.pages_of(70 + T)
+    nb = pages * len(good) + 1
+    g = torch.Generator().manual_seed(B + 1)
+    d["bt"] = torch.full((B, pages), -1, dtype=torch.int32)
+    d["bt"][good] = torch.randperm(nb, generator=g)[1:].int().view(len(good), pages)
+    d["off"] = torch.tensor([0, T] * ((B + 2) // 2), dtype=torch.int32)[:B + 1]
+    d["lens"] = torch.full((B,), 70 + T, dtype=torch.int32)
+    d["pool"] = torch.zeros(nb, 64, 1, 576, dtype=torch.float8_e4m3fn if q8 else torch.bfloat16)
+    d["scales"] = torch.ones(nb, 1) if q8 else None
+    pool, scales, st = _run(d, dev, None)
+    assert st == (ca.MLA_STATUS_BAD_ROW if B > 1 else 0)
+    _check(d, pool, scales, None)  # (the oracle leaves out what falls)
