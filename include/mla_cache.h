@@ -118,7 +118,8 @@ int mla_rope_apply(const mla_rope_dims* dims, const mla_rope_table* table, const
  * Columns are computed in fp32 and rounded once, to bf16 or e4m3.
  *
  * MLA_CACHE_E4M3: the new rows of one page decide its scale, the least power
- * of two 2^e (2^-100 .. 2^119) with every finite |value| <= 448 * 2^e.  A page
+ * of two 2^e (2^-100 .. 2^119) with every finite |value| <= 448 * 2^e; finite values
+ * above 448 * 2^119 (2.98e38) are stored as that, the largest value a page holds.  A page
  * that already holds earlier rows keeps its scale if that is larger; else
  * those rows are moved to the new scale: their exponents shift, and only
  * values that fall below 2^-6 of the new scale are rounded again.  A page's
