@@ -188,7 +188,11 @@ int mla_cache_copy_pages(const mla_cache_dims* dims, int32_t n, const int32_t* s
 
 /* Moves the pages in use to the front of the pool: with `live` pages in use,
  * the k-th of those at or behind `live` goes to the k-th free one before it.
- * Rewrites the rows' entries, the counts and the scales.  workspace is
+ * Rewrites the rows' entries, the counts and the scales.  The table is looked through first: a page that
+ * a row holds although its count is not above 0 (MLA_STATUS_BAD_REF_COUNT) is kept and
+ * moved like one in use, with a count of 0; a length past the table or below 0
+ * (MLA_STATUS_BAD_SEQLEN) is taken as the nearest possible one; an entry outside the pool
+ * (MLA_STATUS_BAD_BLOCK_TABLE) stays as it is.  workspace is
  * mla_cache_compact_workspace_bytes(dims) bytes; its first int32 is `live`
  * afterwards. */
 size_t mla_cache_compact_workspace_bytes(const mla_cache_dims* dims);

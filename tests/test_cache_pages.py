@@ -231,3 +231,74 @@ def test_pages_stream_and_graph(dev):
     graph.replay()
     w.moved(oc.fork([2], [4], w.np["bt"], w.np["lens"], w.np["refs"]))
     w.check()
+
+
+@pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("extra", [0, 3])
+def test_compact_keeps_pages_whose_count_was_lost(dev, extra, q8):
+    """Held pages with a count of 0 (or below), before and behind the border: reported, and kept with their
+    bytes, entries and scales like the others."""
+    lens = [300, 64, 1000, 5, 640]
+    nb = sum(oc.pages_of(n) for n in lens) + 4 + extra
+    w = World(lens, nb, dev, q8, rows=7, seed=31 + extra)
+    w.fork([0, 2], [5, 6])
+    w.free([1, 4])
+    live = int((w.np["refs"] > 0).sum())
+    held = sorted({int(w.np["bt"][b, j]) for b in range(7) for j in range(oc.pages_of(int(w.np["lens"][b])))})
+    assert len(held) == live
+    lost = [held[0], held[2], held[-1]]
+    for value in (0, -3):
+        if value == 0:
+            assert lost[0] < live <= lost[-1]
+        w.refs[torch.tensor(lost, device=dev)] = value
+        w.np["refs"][lost] = 1
+        copies = dict(oc.compact(w.np["bt"], w.np["lens"], w.np["refs"]))
+        w.moved(copies.items())
+        lost = [copies.get(p, p) for p in lost]
+        w.np["refs"][lost] = 0
+        w.status.zero_()
+        ws = ca.cache_compact_workspace(w.pool.shape[0], dev)
+        ca.cache_compact(w.bt, w.lens, w.refs, w.pool, w.scales, workspace=ws, status=w.status)
+        w.check(ca.MLA_STATUS_BAD_REF_COUNT)
+        assert int(ws.view(torch.int32)[0]) == live
+
+
+def test_compact_reports_lengths_past_the_table(dev):
+    for bad in (-1, 64 * 9):
+        w = World([300, 64, 200], 20, dev, seed=17, width=8)
+        w.free([1])
+        w.bt[0, 5:] = w.np["bt"][0, 5:] = -1
+        w.lens[0] = bad
+        w.np["lens"][0] = 0 if bad < 0 else 300
+        # (the pages of a row without a length are counted, and move; its entries are nobody's)
+        w.moved(oc.compact(w.np["bt"], w.np["lens"], w.np["refs"]))
+        w.np["lens"][0] = bad
+        ca.cache_compact(w.bt, w.lens, w.refs, w.pool, w.scales, status=w.status)
+        w.check(bd.MLA_STATUS_BAD_SEQLEN | (bd.MLA_STATUS_BAD_BLOCK_TABLE if bad > 0 else 0))
+
+
+def test_compact_keeps_lost_pages_of_large_books(dev):
+    """More pages than the plan holds in registers: it reads the counts, and the marks, a second time."""
+    nb = 66_000
+    pool = torch.zeros(nb, 64, 1, 576, dtype=torch.uint8, device=dev)
+    pool[:, 0, 0, :4] = torch.arange(nb, dtype=torch.int32, device=dev).view(torch.uint8).view(nb, 4)
+    g = torch.Generator().manual_seed(5)
+    held = torch.randperm(nb, generator=g)[:3000].int()
+    bt, lens = held.view(3, 1000).to(dev), torch.full((3,), 64_000, dtype=torch.int32, device=dev)
+    refs = torch.zeros(nb, dtype=torch.int32)
+    refs[held.long()] = 1
+    lost = held[::7].long()
+    n_bt, n_refs = bt.cpu().numpy().copy(), refs.numpy().copy()
+    refs[lost] = 0
+    copies = dict(oc.compact(n_bt, [64_000] * 3, n_refs))
+    n_refs[[copies.get(int(p), int(p)) for p in lost]] = 0
+    refs, status = refs.to(dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    scales = torch.arange(nb, dtype=torch.float32, device=dev)[:, None].contiguous()
+    ca.cache_compact(bt, lens, refs, pool.view(torch.float8_e4m3fn), scales, status=status)
+    torch.cuda.synchronize()
+    assert int(status) == ca.MLA_STATUS_BAD_REF_COUNT
+    np.testing.assert_array_equal(bt.cpu().numpy(), n_bt)
+    np.testing.assert_array_equal(refs.cpu().numpy(), n_refs)
+    at = bt.view(-1).long()
+    assert torch.equal(pool[at, 0, 0, :4].contiguous().view(torch.int32)[:, 0].cpu(), held)
+    assert torch.equal(scales[at, 0].cpu(), held.float())
