@@ -164,9 +164,10 @@ int mla_cache_append(const mla_cache_dims* dims, int32_t tokens, const void* c_k
  * page, in the order of i, so that both rows may be written on.  Parents are
  * taken as they are before the call: one that is a child of the same call is empty
  * then, and so is its child.  A fork that
- * cannot be made (MLA_STATUS_BAD_ROW; _NO_FREE_PAGE; _BAD_BLOCK_TABLE for its
- * last page) leaves its child empty; a bad entry among the full pages is copied
- * as it is, with that word.  parents and children are device int32 [n], 4-byte
+ * cannot be made (MLA_STATUS_BAD_ROW; _NO_FREE_PAGE; _BAD_BLOCK_TABLE, or _BAD_REF_COUNT
+ * where the count is not above 0, for its last page) leaves its child empty; a bad
+ * entry among the full pages is copied as it is, with that word (and a page's count
+ * rises).  The counts alone say which other pages are free.  parents and children are device int32 [n], 4-byte
  * aligned; workspace is mla_cache_fork_workspace_bytes(n) bytes. */
 size_t mla_cache_fork_workspace_bytes(int32_t n);
 int mla_cache_fork(const mla_cache_dims* dims, int32_t n, const int32_t* parents, const int32_t* children,

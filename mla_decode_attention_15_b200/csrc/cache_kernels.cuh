@@ -618,6 +618,9 @@ inline void launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStrea
     cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);  // (an error is the caller's to collect)
 }
 
+// A page that a row holds although its count says that it is free, while a call works.
+constexpr int kHeldUncounted = INT32_MIN;
+
 // ------------------------------------------------------------------ fork
 constexpr int kForkMax = 1024;
 constexpr int kBookThreads = 1024;
@@ -659,12 +662,22 @@ __global__ void __launch_bounds__(kBookThreads)
     }
     if (i < n && !ok) raise(k.status, MLA_STATUS_BAD_ROW);
     const int last = L / kPage;
-    int src = -1;
+    int src = -1, lost = -1, lost_count = 0;
     if (ok && L % kPage != 0) {
         src = k.bt[(size_t)parent * k.max_blocks + last];
         if ((unsigned)src >= (unsigned)k.num_blocks) {
             raise(k.status, MLA_STATUS_BAD_BLOCK_TABLE);
             ok = false;
+            src = -1;
+        } else if (const int count = k.refs[src]; count <= 0) {
+            // held, but free by its count: not copied, and not given out below
+            raise(k.status, MLA_STATUS_BAD_REF_COUNT);
+            ok = false;
+            if (count != kHeldUncounted) {
+                lost = src;
+                lost_count = count;
+                k.refs[src] = kHeldUncounted;
+            }
             src = -1;
         }
     }
@@ -691,6 +704,7 @@ __global__ void __launch_bounds__(kBookThreads)
         found += total;
     }
     __syncthreads();
+    if (lost >= 0) k.refs[lost] = lost_count;
     int dst = -1;
     if (src >= 0) {
         if (rank < found) {
@@ -731,7 +745,7 @@ __global__ void __launch_bounds__(kCopyThreads)
             const int page = k.bt[(size_t)parent * k.max_blocks + j];
             k.bt[(size_t)child * k.max_blocks + j] = page;
             if ((unsigned)page >= (unsigned)k.num_blocks) raise(k.status, MLA_STATUS_BAD_BLOCK_TABLE);
-            else atomicAdd(k.refs + page, 1);
+            else if (atomicAdd(k.refs + page, 1) <= 0) raise(k.status, MLA_STATUS_BAD_REF_COUNT);
         }
     }
     __threadfence();
@@ -784,9 +798,8 @@ inline size_t compact_workspace_words(int num_blocks) { return kCompactList + 2 
 // The table against the counts, before anything moves: a page that a row holds although its count
 // says that it is free would be written over.  Its count is marked, and the plan takes it for
 // one in use (and puts the 0 back).  Whoever finds it writes the same mark, so the order does
-// not matter.  A CTA takes kCheckEntries entries of a row at a time.  2.3 us on B200 for 40 rows with
-// 6,500 pages, of which the plan's launch hides a part.
-constexpr int kHeldUncounted = INT32_MIN;
+// not matter.  A CTA takes kCheckEntries entries of a row at a time.  It lengthens a compaction on
+// B200 by 1.2 us (of 64 rows, 40 in use); the plan's launch overlaps it.
 constexpr int kCheckEntries = 4 * kMoveThreads;
 __global__ void __launch_bounds__(kMoveThreads) mla_cache_check_kernel(const CacheBooks k, int chunks) {
     griddep_launch_dependents();  // (the plan waits for this grid's end)

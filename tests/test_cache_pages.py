@@ -302,3 +302,33 @@ def test_compact_keeps_lost_pages_of_large_books(dev):
     at = bt.view(-1).long()
     assert torch.equal(pool[at, 0, 0, :4].contiguous().view(torch.int32)[:, 0].cpu(), held)
     assert torch.equal(scales[at, 0].cpu(), held.float())
+
+
+@pytest.mark.parametrize("q8", [True, False])
+def test_fork_looks_at_the_counts_of_its_parents(dev, q8):
+    """A parent's last page that is free by its count is not copied, nor given out to another fork, not even where
+    no other page is free; a full page without a count is shared with a word."""
+    w = World([100, 200, 300, 70], 17, dev, q8, rows=12, seed=41)
+    parents, children = [0, 1, 2, 0, 3], [4, 5, 6, 7, 8]
+    lost = [int(w.np["bt"][0, 1]), int(w.np["bt"][2, 4])]
+    for value in (0, -2):
+        v = World([100, 200, 300, 70], 17, dev, q8, rows=12, seed=41)
+        v.refs[torch.tensor(lost, device=dev)] = value
+        ca.cache_fork(v.t(parents), v.t(children), v.bt, v.lens, v.refs, v.pool, v.scales, status=v.status)
+        v.moved(oc.fork([1, 3], [5, 8], v.np["bt"], v.np["lens"], v.np["refs"]))
+        v.np["refs"][lost] = value
+        v.check(ca.MLA_STATUS_BAD_REF_COUNT)
+    # a pool whose only page with a count of 0 is a parent's own
+    v = World([100, 200], 6, dev, q8, rows=4, seed=42)
+    page = int(v.np["bt"][0, 1])
+    v.refs[page] = 0
+    ca.cache_fork(v.t([0, 1]), v.t([2, 3]), v.bt, v.lens, v.refs, v.pool, v.scales, status=v.status)
+    v.np["refs"][page] = 0
+    v.check(ca.MLA_STATUS_BAD_REF_COUNT | ca.MLA_STATUS_NO_FREE_PAGE)
+    # among the full pages
+    v = World([128, 64], 8, dev, q8, rows=4, seed=43)
+    page = int(v.np["bt"][0, 1])
+    v.refs[page] = v.np["refs"][page] = 0
+    ca.cache_fork(v.t([0, 1]), v.t([2, 3]), v.bt, v.lens, v.refs, v.pool, v.scales, status=v.status)
+    v.moved(oc.fork([0, 1], [2, 3], v.np["bt"], v.np["lens"], v.np["refs"]))
+    v.check(ca.MLA_STATUS_BAD_REF_COUNT)
