@@ -52,12 +52,16 @@ constexpr int kMinScaleExp = -100, kMaxScaleExp = 119;
 // ------------------------------------------------------------------ rotation
 // cos and sin (times the amplitude) of pair i at a position.  The angle in
 // turns is a product of 53-bit numbers, so its fraction is good to 2^-53 of the
-// whole turns: 1e-7 turns are not reached below 2^29 turns.
+// whole turns: 1e-7 turns are not reached below 2^29 turns.  Rounded to fp32 alone that fraction
+// would move a small cosine by 1e-7; what the rounding leaves turns the pair once more, to first order.
 __device__ __forceinline__ float2 rope_cos_sin(const double* turns, float amplitude, int pos, int i) {
     const double t = static_cast<double>(pos) * turns[i];
+    const double half = 2.0 * (t - rint(t));  // half turns
+    const float f = static_cast<float>(half);
+    const float rest = static_cast<float>(half - f) * 3.14159265f;
     float s, c;
-    sincospif(2.0f * static_cast<float>(t - rint(t)), &s, &c);
-    return make_float2(c * amplitude, s * amplitude);
+    sincospif(f, &s, &c);
+    return make_float2(fmaf(-s, rest, c) * amplitude, fmaf(c, rest, s) * amplitude);
 }
 __device__ __forceinline__ void rotate(float& a, float& b, float2 cs) {
     const float x = a * cs.x - b * cs.y, y = a * cs.y + b * cs.x;

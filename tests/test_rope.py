@@ -165,3 +165,26 @@ def test_result_of_another_stream_is_not_shared(dev):
     ca.rope_apply(x, pos, table, offset=128, out=got, stream=s.cuda_stream)
     s.synchronize()
     assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_rope_small_sines_and_cosines(dev, interleaved, transpose):
+    """A unit vector comes out as the cosine and the sine, each right to its own size: two units in the
+    last place of the functions (2^-22), half a unit each for the remainder of the angle and the product
+    with 1 (2^-23 in all), and the angle itself, a 53-bit product on either side (below 2^-50 of the
+    position, in radians)."""
+    T = 20_000
+    pos = torch.randint(0, 1 << 20, (T,), generator=torch.Generator().manual_seed(77), dtype=torch.int64)
+    x = torch.zeros(T, 1, 64)
+    first = torch.arange(0, 64, 2) if interleaved else torch.arange(32)
+    second = first + (1 if interleaved else 32)
+    x[..., first] = 1
+    got = ca.rope_apply(x.to(dev), pos.to(torch.int32).to(dev), ca.make_rope(interleaved=interleaved), transpose=transpose)
+    got = got.cpu().double().numpy()[:, 0]
+    f = oc.frequencies()
+    ang = np.fmod(pos.numpy()[:, None].astype(np.float64) * f, 2 * np.pi)
+    for cols, ref in ((first, np.cos(ang)), (second, np.sin(-ang if transpose else ang))):
+        err = np.abs(got[:, cols.numpy()] - ref)
+        tol = (2.0 ** -22 + 2.0 ** -23) * np.abs(ref) + 2.0 ** -50 * pos.numpy()[:, None]
+        assert (err <= tol).all(), float((err / tol).max())
