@@ -63,9 +63,9 @@ extern "C" {
 
 typedef struct mla_rope_config {
     double theta;                  /* base, > 1 */
-    double factor;                 /* > 0; linear and yarn */
+    double factor;                 /* > 0; linear and yarn (so small that 2^31 f_i is no number: refused) */
     double beta_fast, beta_slow;   /* yarn: > 0 */
-    double amplitude;              /* finite */
+    double amplitude;              /* finite as fp32 */
     int32_t original_max_position; /* yarn: >= 1 */
     int32_t scaling;               /* MLA_ROPE_* */
     int32_t interleaved;           /* 1: pairs (2i, 2i+1); 0: pairs (i, i + 32) */

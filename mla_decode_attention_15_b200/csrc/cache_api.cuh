@@ -249,7 +249,7 @@ int mla_decode_q8_combine(const mla_decode_dims* dims, const void* schedule, con
 
 int mla_rope_init(const mla_rope_config* c, mla_rope_table* t) {
     if (c == nullptr || t == nullptr) return MLA_ERR_INVALID_ARG;
-    if (!std::isfinite(c->theta) || c->theta <= 1.0 || !std::isfinite(c->amplitude) || c->reserved != 0 ||
+    if (!std::isfinite(c->theta) || c->theta <= 1.0 || !std::isfinite((float)c->amplitude) || c->reserved != 0 ||
         c->scaling < MLA_ROPE_NONE || c->scaling > MLA_ROPE_YARN || (c->interleaved != 0 && c->interleaved != 1))
         return MLA_ERR_INVALID_ARG;
     if (c->scaling != MLA_ROPE_NONE && !(std::isfinite(c->factor) && c->factor > 0.0)) return MLA_ERR_INVALID_ARG;
@@ -267,6 +267,7 @@ int mla_rope_init(const mla_rope_config* c, mla_rope_table* t) {
         low = std::fmax(std::floor(pair_of(c->beta_fast)), 0.0);
         high = std::fmin(std::ceil(pair_of(c->beta_slow)), d - 1.0);
     }
+    double turns[kRopePairs];
     for (int i = 0; i < kRopePairs; ++i) {
         double f = std::pow(c->theta, -2.0 * i / d);
         if (c->scaling == MLA_ROPE_LINEAR) f /= c->factor;
@@ -274,8 +275,11 @@ int mla_rope_init(const mla_rope_config* c, mla_rope_table* t) {
             const double r = std::fmin(std::fmax((i - low) / std::fmax(high - low, 0.001), 0.0), 1.0);
             f = f * (1.0 - r) + f / c->factor * r;
         }
-        t->turns[i] = f / kTwoPi;
+        turns[i] = f / kTwoPi;
+        // the angle of every position is a number
+        if (!std::isfinite(turns[i] * 2147483648.0)) return MLA_ERR_INVALID_ARG;
     }
+    for (int i = 0; i < kRopePairs; ++i) t->turns[i] = turns[i];
     t->amplitude = (float)c->amplitude;
     t->interleaved = c->interleaved;
     return MLA_OK;

@@ -289,3 +289,13 @@ def test_oracle_rotation_keeps_lengths_and_offsets():
     a, b = np.random.RandomState(2).randn(2, 1, 64)
     s = [float((oc.rotate(a, [p + 5]) * oc.rotate(b, [p])).sum()) for p in (0, 3, 1000)]
     np.testing.assert_allclose(s, s[0], rtol=1e-9)
+
+
+@pytest.mark.parametrize("kw", [dict(amplitude=1e39), dict(amplitude=-1e300), dict(scaling="linear", factor=1e-308),
+                                dict(scaling="linear", factor=5e-324), dict(scaling="yarn", factor=1e-305)])
+def test_rope_tables_that_hold_no_numbers_are_refused(lib, kw):
+    """An amplitude that is infinite in fp32, and frequencies by which an angle would be."""
+    with pytest.raises(bd.MlaDecodeError):
+        ca.make_rope(**kw)
+    ca.make_rope(amplitude=3e38)
+    ca.make_rope(scaling="linear", factor=1e-200)
