@@ -46,7 +46,7 @@
 //     plain copy.  A steady step keeps up with the loads; the rest is the first
 //     items' Q split and last items' epilogue, the combine (7 us by itself), and the
 //     clock, which the power limit lowers in a long run.
-//   - 32 requests x 8-32K x 2 tokens x 128 heads, 365 GFLOP on 395 MB: 555 us, 0.66 PFLOP/s of
+//   - 32 requests x 8-32K x 2 tokens x 128 heads, 365 GFLOP on 395 MB: 562 us, 0.65 PFLOP/s of
 //     the sums as defined (0.40 of the measured bf16 rate).  A step's
 //     tensor work (two Q terms, three P terms of 32 columns) is 1,760 cycles; its softmax,
 //     a chain of TMEM read, exponentials, three conversions and the store of P^T,

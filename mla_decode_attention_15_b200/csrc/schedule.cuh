@@ -41,6 +41,9 @@ constexpr int kItemOverhead = 1;   // units charged per (request, head group)
 // tokens x 1-16K 43.8 / 40.6 / 39.5 / 39.3 / 42.2 / 42.6; 16 x 64K 125.6 / 123.8
 // / 121.4 / 121.2 / 121.5 / 124.9; 1 x 1K 13.9 / 12.3 / 12.2 / 12.1 / 12.0 / 12.0
 // (its 16 pages then start on even units, so that no range holds an odd page).
+// More columns, for 1 / 3 / 6 / 12 units: 32 x 2 tokens x 200-8K x 32 heads (2 groups a range) 55.4 /
+// 51.9 / 49.3 / 49.0; 16 x 2 x 1-16K x 20 heads 61.4 / 59.6 / 57.8 / 58.8; 8 x 200-4K x 128 heads
+// (4 groups) 29.1 / 27.7 / 26.1 / 25.7; 32 x 2 x 8-32K x 128 heads (8 groups) 568 / 567 / 567 / 567.
 // The functions below take the overhead as `ov`.  It may exceed a range: that
 // CTA's range is then empty.
 constexpr int kQ8ItemOverhead = 6;
