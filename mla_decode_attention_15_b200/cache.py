@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 from typing import Optional, Tuple
 
 import torch
@@ -490,6 +491,22 @@ def absorbed_mla_step(q_in: torch.Tensor, c_kv: torch.Tensor, k_pe: torch.Tensor
     if q_in.dim() != 4:
         _fail("q_in must be [B, s_q, h, 192]")
     B, s_q, h, width = q_in.shape
+    # What a later part would refuse is refused here, before rows are written into the cache.
+    d, device = decoder.dims, kv_cache.device
+    if isinstance(decoder, Q8Decoder) != (kv_scales is not None):
+        _fail("an 8-bit cache and its scales go with a Q8Decoder, a bf16 cache with an MlaDecoder")
+    if (B, s_q, h, width) != (d.batch, d.s_q, d.num_heads, bd.ABSORB_D_NOPE + bd.ABSORB_D_ROPE):
+        _fail("q_in must be [B, s_q, h, 192] of the decoder's sizes")
+    if kv_cache.shape[0] != d.num_blocks or block_table.shape != (B, d.max_blocks_per_seq) or decoder.out.device != device:
+        _fail("kv_cache and block_table must have the decoder's sizes and device")
+    if decoder.out.dtype is not _BF16:
+        _fail("the decoder's output must be bf16")
+    if q_in.dtype is not _BF16:
+        _fail("q_in must be bf16")
+    bd._bf16_on(w_uk, (h, bd.ABSORB_D_NOPE, bd.ABSORB_D_LATENT), "w_uk", device)
+    bd._bf16_on(w_uv, (h, bd.ABSORB_D_LATENT, bd.ABSORB_D_V_HEAD), "w_uv", device)
+    if not math.isfinite(softmax_scale):
+        _fail("softmax_scale must be finite")
     q = rope_apply(q_in.reshape(B * s_q, h, width), positions, rope, offset=bd.ABSORB_D_NOPE).view(q_in.shape)
     cache_append(c_kv, k_pe, new_offsets, block_table, cache_seqlens, kv_cache, kv_scales, rope, status)
     q_lat = bd.absorb_q(q, w_uk)

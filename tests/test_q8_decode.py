@@ -665,3 +665,35 @@ def test_large_scores_that_rise_a_little(dev, h, exponent, rise, q):
     err = (out[0, 0].cpu().double() - w @ k[:, :512]).abs()
     tol = (2.0 ** -12 + 2.0 ** -18) * (w @ k[:, :512].abs()) + 2.0 ** -22 * len(k) * 448 * w.amax(-1)[:, None]
     assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.parametrize("q8", [True, False])
+def test_absorbed_step_refuses_before_it_writes(dev, q8):
+    """A call that any of its parts would refuse leaves the cache as it was."""
+    B, h, nb = 2, 16, 8
+    d = build([64], 1, 1, seed=45, spare=nb - 1)
+    kv, scales = (d["kv"] if q8 else wide(d)).to(dev), d["scales"].to(dev) if q8 else None
+    r = lambda *s: torch.randn(*s, device=dev).bfloat16()  # noqa: E731
+    make = lambda cls, *a, **k: cls(B, 1, h, nb, 4, False, 0, dev, *a, **k)  # noqa: E731
+    mine, other = (ca.Q8Decoder, bd.MlaDecoder) if q8 else (bd.MlaDecoder, ca.Q8Decoder)
+    dec = make(mine, inline_plan=True)
+    lens = torch.tensor([70, 3], dtype=torch.int32, device=dev)
+    dec.plan(lens)
+    good = dict(q_in=r(B, 1, h, 192), c_kv=r(B, 512), k_pe=r(B, 64), positions=lens - 1,
+                new_offsets=torch.arange(B + 1, dtype=torch.int32, device=dev), w_uk=r(h, 128, 512), w_uv=r(h, 512, 128), rope=ca.make_rope(),
+                block_table=torch.arange(nb, dtype=torch.int32, device=dev).view(B, 4), cache_seqlens=lens, kv_cache=kv,
+                kv_scales=scales, softmax_scale=SCALE, decoder=dec)
+    before, sc = kv.clone(), None if scales is None else scales.clone()
+    bad = [dict(w_uk=good["w_uk"][:, :64].contiguous()), dict(w_uk=good["w_uk"].float()), dict(w_uv=good["w_uv"][:8]), dict(w_uv=good["w_uk"]),
+           dict(w_uv=good["w_uv"].cpu()), dict(softmax_scale=float("inf")), dict(softmax_scale=float("nan")), dict(decoder=make(other)),
+           dict(decoder=make(mine, fp32_out=True)), dict(decoder=mine(B, 1, h, nb + 1, 4, False, 0, dev)),
+           dict(decoder=mine(B, 1, h, nb, 5, False, 0, dev)), dict(decoder=mine(B, 1, h + 1, nb, 4, False, 0, dev)),
+           dict(q_in=good["q_in"][:1]), dict(q_in=r(B, 1, h, 256)), dict(q_in=good["q_in"].float())]
+    for change in bad:
+        with pytest.raises((ValueError, bd.MlaDecodeError)):
+            ca.absorbed_mla_step(**dict(good, **change))
+    torch.cuda.synchronize()
+    assert torch.equal(kv.view(torch.uint8), before.view(torch.uint8)) and (sc is None or torch.equal(scales, sc))
+    ca.absorbed_mla_step(**good)
+    torch.cuda.synchronize()
+    assert dec.status() == 0 and not torch.equal(kv.view(torch.uint8), before.view(torch.uint8))
