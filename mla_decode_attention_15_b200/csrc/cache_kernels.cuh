@@ -576,7 +576,7 @@ inline void launch_append(const AppendParams& p, cudaStream_t stream) {
 // ------------------------------------------------------------------ page moves
 // A CTA moves slices of pages, two 16-byte loads in flight per thread; 288 threads cut
 // a page (36,864 or 73,728 bytes) into 4 or 8 whole slices.  Bound by the bytes, each
-// read and written once; a compaction that moves 182 MB takes 31 us (5.9 TB/s).
+// read and written once; a compaction that moves 182 MB takes 29.5 us (6.2 TB/s).
 constexpr int kCopyThreads = 288;
 constexpr int kSliceBytes = 2 * kCopyThreads * 16;
 static_assert(kPage * kDqk % kSliceBytes == 0, "whole slices");
@@ -638,8 +638,8 @@ __host__ __device__ inline size_t fork_workspace_words(int n) { return (size_t)k
 
 // One CTA decides every fork, in order: checks the rows, ranks the forks that need
 // a page and hands them the lowest free ones.  Which pages are free depends on every
-// fork before, so one block settles it; a chain of short reads and block scans, 6 us on B200 for
-// 24 forks in 350 pages and 8 us for 192 in 5,200, while the copy kernel is being launched.
+// fork before, so one block settles it; a chain of short reads and block scans, 6.8 us on B200 for
+// 24 forks in 350 pages and 8.8 us for 192 in 5,200, while the copy kernel is being launched.
 __global__ void __launch_bounds__(kBookThreads)
     mla_cache_fork_plan_kernel(const CacheBooks k, int n, const int32_t* parents, const int32_t* children, int32_t* ws) {
     __shared__ __align__(16) int child_s[kForkMax];
@@ -838,7 +838,7 @@ __global__ void __launch_bounds__(kMoveThreads) mla_cache_check_kernel(const Cac
 // pages that move or are moved to numbers both lists.  A warp owns a run of
 // consecutive pages, 32 at a time, and a lane keeps which of its pages are in use as
 // bits, so the counts are read once up to 65,536 pages (again for more), and
-// only the warps' totals meet across the block.  9 us on B200 for 10,500 pages (two rounds
+// only the warps' totals meet across the block.  8.3 us on B200 for 10,500 pages (two rounds
 // of loads, three block scans); 16 loads in flight instead of 8 measured the same.
 constexpr int kPlanBits = 64;
 __global__ void __launch_bounds__(kBookThreads) mla_cache_compact_plan_kernel(const CacheBooks k, int32_t* ws) {

@@ -51,7 +51,7 @@
 //     tensor work (two Q terms, three P terms of 32 columns) is 1,760 cycles; its softmax,
 //     a chain of TMEM read, exponentials, three conversions and the store of P^T,
 //     about 2,950.
-//   - 16 requests x 1-16K x 2 tokens x 16 heads, 81 MB: 39 us; 1 x 1K: 11.4 us.  An item's
+//   - 16 requests x 1-16K x 2 tokens x 16 heads, 81 MB: 39 us; 1 x 1K: 11.3 us.  An item's
 //     fixed parts: plan, Q split, first step, epilogue, combine.
 #pragma once
 
