@@ -805,21 +805,21 @@ inline size_t compact_workspace_words(int num_blocks) { return kCompactList + 2 
 // The table against the counts, before anything moves: a page that a row holds although its count
 // says that it is free would be written over.  Its count is marked, and the plan takes it for
 // one in use (and puts the 0 back).  Whoever finds it writes the same mark, so the order does
-// not matter.  A CTA takes kCheckEntries entries of a row at a time.  It lengthens a compaction on
-// B200 by 1.2 us (of 64 rows, 40 in use); the plan's launch overlaps it.
+// not matter.  CTA (x, y) takes every gridDim.y-th piece of kCheckEntries entries of row x: several to a row only while
+// rows alone do not fill the device, and none costs more than its length's read where a wide table is mostly empty.  It
+// lengthens a compaction on B200 by 1.2 us (of 64 rows, 40 in use); the plan's launch overlaps it.
 constexpr int kCheckEntries = 4 * kMoveThreads;
-__global__ void __launch_bounds__(kMoveThreads) mla_cache_check_kernel(const CacheBooks k, int chunks) {
+__global__ void __launch_bounds__(kMoveThreads) mla_cache_check_kernel(const CacheBooks k) {
     griddep_launch_dependents();  // (the plan waits for this grid's end)
-    for (int64_t u = blockIdx.x; u < (int64_t)k.batch * chunks; u += gridDim.x) {
-        const int b = (int)(u / chunks), first = (int)(u - (int64_t)b * chunks) * kCheckEntries;
-        const int L = k.lens[b];
-        if (first == 0 && threadIdx.x == 0 && !seqlen_in_range(L, k.max_blocks)) raise(k.status, MLA_STATUS_BAD_SEQLEN);
-        const int end = min(pages_of(clamp_seqlen(L, k.max_blocks)), first + kCheckEntries);
-        const int32_t* bt = k.bt + (size_t)b * k.max_blocks;
+    const int b = blockIdx.x, L = k.lens[b];
+    if (blockIdx.y == 0 && threadIdx.x == 0 && !seqlen_in_range(L, k.max_blocks)) raise(k.status, MLA_STATUS_BAD_SEQLEN);
+    const int end = pages_of(clamp_seqlen(L, k.max_blocks));
+    const int32_t* bt = k.bt + (size_t)b * k.max_blocks;
+    for (int64_t first = (int64_t)blockIdx.y * kCheckEntries; first < end; first += (int64_t)gridDim.y * kCheckEntries) {
         int page[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int j = first + i * kMoveThreads + threadIdx.x;
+            const int64_t j = first + i * kMoveThreads + threadIdx.x;
             page[i] = j < end ? bt[j] : -1;
         }
 #pragma unroll
@@ -961,8 +961,8 @@ __global__ void __launch_bounds__(kCopyThreads)
 }
 inline void launch_compact(const CacheBooks& k, const CachePool& pool, int32_t* ws, cudaStream_t stream) {
     const int slices = page_slices(pool.page_bytes);
-    const int chunks = (k.max_blocks + kCheckEntries - 1) / kCheckEntries;
-    mla_cache_check_kernel<<<(unsigned)min((int64_t)148 * 8, (int64_t)k.batch * chunks), kMoveThreads, 0, stream>>>(k, chunks);
+    const int pieces = (k.max_blocks + kCheckEntries - 1) / kCheckEntries;
+    mla_cache_check_kernel<<<dim3(k.batch, min(pieces, max(1, 148 * 8 / k.batch))), kMoveThreads, 0, stream>>>(k);
     launch_after(mla_cache_compact_plan_kernel, dim3(1), kBookThreads, stream, k, ws);
     const int64_t most = max((int64_t)k.batch, (int64_t)(k.num_blocks / 2) * slices);
     launch_after(mla_cache_compact_kernel, dim3((unsigned)min((int64_t)148 * 24, max(most, (int64_t)1))), kCopyThreads, stream, k, pool,

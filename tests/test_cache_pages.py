@@ -332,3 +332,36 @@ def test_fork_looks_at_the_counts_of_its_parents(dev, q8):
     ca.cache_fork(v.t([0, 1]), v.t([2, 3]), v.bt, v.lens, v.refs, v.pool, v.scales, status=v.status)
     v.moved(oc.fork([0, 1], [2, 3], v.np["bt"], v.np["lens"], v.np["refs"]))
     v.check(ca.MLA_STATUS_BAD_REF_COUNT)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 1500])
+def test_compact_finds_lost_pages_far_into_a_row(dev, rows):
+    """Rows of several thousand entries, alone and among more rows than the device has room for."""
+    nb, n, width = 4600, 2200, 5000
+    g = torch.Generator().manual_seed(rows)
+    held = torch.randperm(nb, generator=g)[:2 * n].int().view(2, n)
+    bt = torch.full((rows, width), -1, dtype=torch.int32)
+    lens = torch.zeros(rows, dtype=torch.int32)
+    at = [rows // 2, rows - 1][:min(rows, 2)]
+    for i, b in enumerate(at):
+        bt[b, :n], lens[b] = held[i], 64 * n - 13
+    held = held[:len(at)].flatten()
+    refs = torch.zeros(nb, dtype=torch.int32)
+    refs[held.long()] = 1
+    lost = held[[0, 1023, 1024, 2047, 2048, n - 1, len(held) - 1]].long()
+    n_bt, n_refs = bt.numpy().copy(), refs.numpy().copy()
+    refs[lost] = 0
+    copies = dict(oc.compact(n_bt, lens.tolist(), n_refs))
+    n_refs[[copies.get(int(p), int(p)) for p in lost]] = 0
+    pool = torch.zeros(nb, 64, 1, 576, dtype=torch.uint8, device=dev)
+    pool[:, 0, 0, :4] = torch.arange(nb, dtype=torch.int32, device=dev).view(torch.uint8).view(nb, 4)
+    scales, status = torch.arange(nb, dtype=torch.float32, device=dev)[:, None].contiguous(), torch.zeros(1, dtype=torch.int32, device=dev)
+    bt, refs = bt.to(dev), refs.to(dev)
+    ca.cache_compact(bt, lens.to(dev), refs, pool.view(torch.float8_e4m3fn), scales, status=status)
+    torch.cuda.synchronize()
+    assert int(status) == ca.MLA_STATUS_BAD_REF_COUNT
+    np.testing.assert_array_equal(bt.cpu().numpy(), n_bt)
+    np.testing.assert_array_equal(refs.cpu().numpy(), n_refs)
+    now = torch.cat([bt[b, :n] for b in at]).long()
+    assert torch.equal(pool[now, 0, 0, :4].contiguous().view(torch.int32)[:, 0].cpu(), held)
+    assert torch.equal(scales[now, 0].cpu(), held.float())
